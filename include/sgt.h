@@ -67,7 +67,14 @@ typedef enum sgt_status {
   SGT_ENOMEM = -5         /* context creation could not allocate               */
 } sgt_status;
 
-enum sgt_dtype { SGT_F32 = 0, SGT_BF16 = 1 };
+enum sgt_dtype {
+  SGT_F32 = 0,
+  SGT_BF16 = 1,
+  SGT_F8E4M3 = 2  /* OCP e4m3: an output of sgt_rms_norm only */
+};
+
+/* Scores of sgt_moe_gate. */
+enum sgt_score { SGT_SCORE_SOFTMAX = 0, SGT_SCORE_SIGMOID = 1 };
 
 /* Storage of the K x N right-hand matrix: row-major K x N, or row-major N x K
  * (the same matrix transposed, as a Linear layer stores its weight). */
@@ -574,6 +581,121 @@ SGT_API int64_t sgt_trace_words(int W, int64_t M, int64_t K, int64_t N, const sg
  * each signal tile of the local block (tile-row-major) cut into row bands of
  * 32 rows (the whole tile when rs_tile <= 32), band-minor. */
 SGT_API int64_t sgt_rs_trace_words(int W, int64_t M, int64_t N, const sgt_opts* opts);
+
+/*
+ * ---- Operators of the layer between the products ----
+ *
+ * What a tensor- or expert-parallel layer computes between the products and
+ * collectives above: the norm in front of an AllGather, the router in front of
+ * an AllToAll, and the attention between two products (the pages measure
+ * prefill and decode attention modules and flash decoding beside the GEMMs).
+ * These calls take no context, flags or options and keep no state: each runs on
+ * the calling thread's current device, asynchronously on `stream` (they may be
+ * captured into a graph), and calls on different streams may overlap as long as
+ * they share no buffer that either writes.  Values are computed in fp32 and
+ * rounded once, to nearest even, when stored.  Strides are in elements.
+ */
+
+/*
+ * RMS norm with the residual's addition, over T rows of H elements:
+ *     s = x + residual
+ *     sum_out = s
+ *     y = s / sqrt(mean(s^2) + eps) * weight      (of s before sum_out's rounding)
+ *     out = y, or (SGT_F8E4M3) e4m3(y / scale) with scale = max(max |y| / 448, 2^-126) over
+ *           the row (block 0) or over each block of 128 columns (block 128, the last ragged)
+ * x: T rows, x_stride apart (>= H), x_dtype SGT_F32 or SGT_BF16.  residual,
+ *     sum_out: T x H dense, r_dtype; either may be NULL (s = x; s not stored).
+ *     sum_out may be residual.  weight: H, w_dtype.
+ * out: T x H dense, SGT_F32, SGT_BF16 or SGT_F8E4M3; it may be x when it has x's
+ *     type and x_stride is H.  No other buffers may overlap.
+ * scales: fp32, T (block 0) or T x ceil(H / 128); NULL unless out is 8-bit.
+ * A row with a NaN or infinity gives NaN where the formula does.
+ * Requirements: 1 <= H <= 65536; buffers aligned to their elements (16-byte
+ *     aligned rows are read and written 16 bytes at a time).  T = 0: no-op.
+ */
+SGT_API sgt_status sgt_rms_norm(const void* x, int x_dtype, int64_t x_stride, const void* residual, void* sum_out,
+                                int r_dtype, const void* weight, int w_dtype, void* out, int out_dtype, float* scales,
+                                int block, int64_t T, int64_t H, float eps, void* stream);
+
+/*
+ * Routing of T tokens to topk of E experts, for sgt_a2a_dispatch and
+ * sgt_a2a_combine:
+ *     score = softmax(logits) or 1 / (1 + exp(-logits))
+ *     choice = score + bias, or without a bias the logit (which orders alike)
+ *     topk_ids[t] = the topk experts of largest choice, largest first, of equal
+ *           ones the lower id; with n_group > 1 only among the experts of the topk_group
+ *           groups (of E / n_group consecutive experts) with the largest sum of their
+ *           group_top largest score + bias (of equal ones the lower group)
+ *     gate[t] = score of those experts (without the bias), divided by their sum if
+ *           `renormalize`, times `scale`
+ * logits: T rows, `stride` apart (>= E), SGT_F32 or SGT_BF16.  A NaN logit counts as -infinity
+ *     (score 0); a row of -infinity alone has scores 0, and gates 0 also when renormalised.
+ * bias: E fp32, or NULL (a NaN in it counts as -infinity).  topk_ids: T x topk int32; gate: T x topk fp32.
+ * Requirements: E <= 1024, topk <= min(E, 64), n_group a divisor of E of at most
+ *     64, topk <= topk_group * E / n_group, group_top 1 or 2.  T = 0: no-op.
+ */
+SGT_API sgt_status sgt_moe_gate(const void* logits, int dtype, int64_t stride, const float* bias, int32_t* topk_ids,
+                                float* gate, int64_t T, int E, int topk, int score, int n_group, int topk_group,
+                                int group_top, int renormalize, float scale, void* stream);
+
+/*
+ * Attention over whole prompts: n_seqs sequences packed one after another.
+ * Sequence s holds queries cu_q[s] .. cu_q[s+1]-1 and keys cu_k[s] ..
+ * cu_k[s+1]-1 (Lq and Lk of them); query head h reads key head h / (Hq / Hkv):
+ *     out = softmax(scale * q k^T + mask) v,   lse = log(sum(exp(scale * q k^T + mask)))
+ * With `causal`, query i of a sequence sees its keys 0 .. i + Lk - Lq (so a
+ * later piece of a prompt sees all that came before it); else it sees all Lk.
+ * A query that sees no key gets out = 0 and lse = -infinity.  What a query does
+ * not see does not reach its output, whatever it holds (NaN included).
+ * q: total_q tokens of Hq heads of D bf16, k and v: total_k tokens of Hkv
+ *     heads; head h of token t at t * token stride + h * head stride, so slices
+ *     of one product's output can be passed as they are.
+ * out: total_q x Hq x D bf16, dense.  lse: total_q x Hq fp32, or NULL.
+ * cu_q, cu_k: n_seqs + 1 ascending int32 in device memory, within [0, total]
+ *     (values outside are cut to it).  Rows of out in no sequence are not written.
+ * Scores and sums are fp32; the weights exp(...) are rounded to bf16 for the
+ *     product with v, as the matrix cores take them.
+ * Requirements: D 64 or 128; strides multiples of 8, token strides below 2^24;
+ *     q, k, v, out 16-byte aligned; Hq a multiple of Hkv, at most 1024.
+ */
+SGT_API sgt_status sgt_attn_prompt(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                                   int64_t k_head, const void* v, int64_t v_token, int64_t v_head, void* out, float* lse,
+                                   const int32_t* cu_q, const int32_t* cu_k, int n_seqs, int64_t total_q,
+                                   int64_t total_k, int Hq, int Hkv, int D, int causal, float scale, void* stream);
+
+/*
+ * Attention of one new token of each of B sequences over a paged cache (flash
+ * decoding: the work is split over the caches' length and joined).  Sequence b
+ * sees its first seq_lens[b] cached tokens; token j lies in page
+ * block_table[b][j / page_size], slot j % page_size:
+ *     out[b, h] = softmax(scale * q[b, h] k^T) v,  lse[b, h] = log(sum(exp(scale * q[b, h] k^T)))
+ * With `out` in fp32 and lse, shares of a sequence held by several ranks can be
+ * joined: out = sum_r exp(lse_r - lse) out_r, lse = log(sum_r exp(lse_r)).
+ * q: B tokens q_stride apart, Hq x D bf16 each.  k_cache, v_cache: n_pages pages
+ *     of page_size slots of Hkv heads of D bf16, both with the same page, slot
+ *     and head strides, in either order of slots and heads.
+ * block_table: B rows of max_pages int32, table_stride apart.  Tokens on a page
+ *     outside [0, n_pages) are not seen.  seq_lens: B int32; 0 (or less) gives
+ *     out = 0 and lse = -infinity; more than max_pages * page_size is cut to it.
+ *     Slots past a sequence's length are not seen, whatever they hold.
+ * out: B x Hq x D dense, SGT_BF16 or SGT_F32.  lse: B x Hq fp32, or NULL.
+ * workspace: sgt_attn_decode_workspace_bytes() bytes, 16-byte aligned, zeroed
+ *     once before its first use; the call leaves it ready for the next one.  Calls that may
+ *     overlap in time need one each.
+ * Results do not depend on timing: the same inputs give the same bits.
+ * Requirements: D 64 or 128; strides multiples of 8; 16-byte aligned q, caches,
+ *     out; Hq a multiple of Hkv, at most 1024; B * Hkv <= 2^24; 1 <= page_size
+ *     <= 2^20, max_pages * page_size < 2^31.
+ */
+SGT_API sgt_status sgt_attn_decode(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                   int64_t page_stride, int64_t slot_stride, int64_t head_stride, int64_t n_pages,
+                                   int page_size, const int32_t* block_table, int64_t table_stride, int max_pages,
+                                   const int32_t* seq_lens, void* out, int out_dtype, float* lse, void* workspace,
+                                   int64_t workspace_bytes, int B, int Hq, int Hkv, int D, float scale, void* stream);
+
+/* Bytes of the workspace of an sgt_attn_decode call (whatever the lengths), or
+ * a negative status for invalid arguments. */
+SGT_API int64_t sgt_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int D);
 
 #ifdef __cplusplus
 }

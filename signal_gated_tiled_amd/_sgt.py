@@ -16,12 +16,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsgt.so")
 
 SGT_OK, SGT_EINVAL, SGT_EUNSUPPORTED, SGT_ETIMEDOUT, SGT_EHIP, SGT_ENOMEM = 0, -1, -2, -3, -4, -5
-SGT_F32, SGT_BF16 = 0, 1
+SGT_F32, SGT_BF16, SGT_F8E4M3 = 0, 1, 2
 SGT_KN, SGT_NK = 0, 1
 PRODUCERS = {"cu": 0, "preset": 1, "serial": 2, "sdma": 3}
 ORDERS = {"mesh": 0, "shard": 1}
 LAYOUTS = {"kn": SGT_KN, "nk": SGT_NK}
 ARRIVALS = {"inorder": 0, "per_peer": 1, "global": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class SgtError(RuntimeError):
@@ -106,12 +107,22 @@ def lib() -> ctypes.CDLL:
         L.sgt_rs_trace_words.argtypes = [ctypes.c_int, I64, I64, ctypes.POINTER(Opts)]
         L.sgt_rs_trace_words.restype = I64
         L.sgt_gemm_rs_static.argtypes = [P, P, P, P, P, ctypes.c_int, I64, I64, I64, ctypes.POINTER(Opts), P]
+        CI, F = ctypes.c_int, ctypes.c_float
+        L.sgt_rms_norm.argtypes = [P, CI, I64, P, P, CI, P, CI, P, CI, P, CI, I64, I64, F, P]
+        L.sgt_moe_gate.argtypes = [P, CI, I64, P, P, P, I64, CI, CI, CI, CI, CI, CI, CI, F, P]
+        L.sgt_attn_prompt.argtypes = [P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, P, CI, I64, I64, CI, CI, CI, CI,
+                                      F, P]
+        L.sgt_attn_decode.argtypes = [P, I64, P, P, I64, I64, I64, I64, CI, P, I64, CI, P, P, CI, P, P, I64, CI, CI,
+                                      CI, CI, F, P]
+        L.sgt_attn_decode_workspace_bytes.argtypes = [CI, CI, CI, CI]
+        L.sgt_attn_decode_workspace_bytes.restype = I64
         L.sgt_gemm_rs_static_scratch_bytes.argtypes = []
         L.sgt_gemm_rs_static_scratch_bytes.restype = I64
         for f in ("sgt_ctx_create", "sgt_ctx_destroy", "sgt_sync", "sgt_ag_gemm", "sgt_rs_flag_count", "sgt_gemm_rs",
                   "sgt_gemm_rs_paced", "sgt_moe_ag_gemm", "sgt_moe_gemm_rs",
                   "sgt_moe_gemm_rs_paced", "sgt_allgather", "sgt_ll_allgather", "sgt_ring_allreduce",
-                  "sgt_a2a_dispatch", "sgt_a2a_combine", "sgt_gemm_rs_static"):
+                  "sgt_a2a_dispatch", "sgt_a2a_combine", "sgt_gemm_rs_static", "sgt_rms_norm", "sgt_moe_gate",
+                  "sgt_attn_prompt", "sgt_attn_decode"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -299,6 +310,151 @@ def gemm_rs_static(A_local, B, partials: Sequence, partial_out, C_shard, *, stre
 
 def gemm_rs_static_scratch_bytes() -> int:
     return int(lib().sgt_gemm_rs_static_scratch_bytes())
+
+
+def _layer_ptr(t, name: str, dtype, shape=None, device=None) -> int:
+    """Device pointer of a dense tensor of this dtype (and shape) on `device`; None is NULL."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    return _dev_ptr(t, name, device)
+
+
+def _current_device(t, name: str):
+    """The device of `t`, which must be the calling thread's current GPU (the layer operators run there)."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if torch.cuda.current_device() != t.device.index:
+        raise ValueError("the call runs on the current device (%d); %s is on %s" %
+                         (torch.cuda.current_device(), name, t.device))
+    return t.device
+
+
+def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: float = 1e-6, stream=None):
+    """RMS norm with the residual's addition (sgt_rms_norm): s = x + residual, sum_out = s, out = s / sqrt(mean(s^2) +
+    eps) * weight.  x: T x H fp32 or bf16, rows may be strided; weight: H; residual, sum_out: T x H of one dtype, either
+    may be None; out: T x H bf16, fp32 or float8_e4m3fn, the last with fp32 scales: T x 1 (one per row) or
+    T x ceil(H / 128) (one per 128 columns)."""
+    import torch
+    dev = _current_device(x, "x")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be T x H with contiguous rows")
+    T, H = x.shape
+    r = residual if residual is not None else sum_out
+    r_type = r.dtype if r is not None else x.dtype
+    if out.dtype == torch.float8_e4m3fn:
+        if scales is None or scales.dim() != 2:
+            raise ValueError("an 8-bit output needs scales of T x 1 or T x ceil(H / 128)")
+        out_code, block = SGT_F8E4M3, 0 if scales.shape[1] == 1 else 128
+        s_shape = (T, 1 if block == 0 else -(-H // 128))
+    else:
+        out_code, block, s_shape = _dtype_code(out), 0, None
+    _check(lib().sgt_rms_norm(x.data_ptr(), _dtype_code(x), x.stride(0) if T > 1 else max(H, 1),
+                              _layer_ptr(residual, "residual", r_type, (T, H), dev),
+                              _layer_ptr(sum_out, "sum_out", r_type, (T, H), dev),
+                              SGT_BF16 if r_type == torch.bfloat16 else SGT_F32,
+                              _layer_ptr(weight, "weight", weight.dtype, (H,), dev), _dtype_code(weight),
+                              _layer_ptr(out, "out", out.dtype, (T, H), dev), out_code,
+                              _layer_ptr(scales, "scales", torch.float32, s_shape, dev), block, T, H, eps,
+                              _stream_handle(stream)))
+
+
+def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_group: int = 1, topk_group: int = 1,
+             group_top: int = 2, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Routing of tokens to experts (sgt_moe_gate).  logits: T x E fp32 or bf16, rows may be strided; topk_ids: T x k
+    int32 and gate: T x k fp32, written, as a2a_dispatch and a2a_combine take them; bias: E fp32, added to the scores
+    for the choice only; score: 'softmax' or 'sigmoid'; with n_group > 1 the experts come from the topk_group groups of
+    largest sum of their group_top largest scores (with the bias)."""
+    import torch
+    dev = _current_device(logits, "logits")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be T x E with contiguous rows")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    if n_group == 1:
+        group_top = 1
+    _check(lib().sgt_moe_gate(logits.data_ptr(), _dtype_code(logits), logits.stride(0) if T > 1 else max(E, 1),
+                              _layer_ptr(bias, "bias", torch.float32, (E,), dev),
+                              _layer_ptr(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+                              _layer_ptr(gate, "gate", torch.float32, (T, k), dev), T, E, k, SCORES[score], n_group,
+                              topk_group, group_top, 1 if renormalize else 0, scale, _stream_handle(stream)))
+
+
+def _heads(t, name: str, dev):
+    """(pointer, token stride, head stride) of a bf16 tokens x heads x D tensor with contiguous heads."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1:
+        raise ValueError("%s must be tokens x heads x D with contiguous heads" % name)
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else 0, st[1] if t.shape[1] > 1 else 0
+
+
+def attn_prompt(q, k, v, out, cu_q, cu_k, *, lse=None, causal: bool = True, scale: Optional[float] = None, stream=None):
+    """Attention over packed prompts (sgt_attn_prompt).  q: total_q x Hq x D, k and v: total_k x Hkv x D, bf16, any
+    token and head strides (slices of one QKV tensor can be passed); out: total_q x Hq x D bf16; cu_q, cu_k: int32
+    offsets of the sequences (n_seqs + 1); lse: total_q x Hq fp32 or None; scale: 1 / sqrt(D) by default."""
+    import torch
+    dev = _current_device(q, "q")
+    qp, kp, vp = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
+    total_q, Hq, D = q.shape
+    total_k, Hkv = k.shape[0], k.shape[1]
+    if tuple(k.shape) != tuple(v.shape) or k.shape[2] != D:
+        raise ValueError("k %s and v %s do not match q %s" % (tuple(k.shape), tuple(v.shape), tuple(q.shape)))
+    n = cu_q.shape[0] - 1
+    _check(lib().sgt_attn_prompt(*qp, *kp, *vp, _layer_ptr(out, "out", torch.bfloat16, (total_q, Hq, D), dev),
+                                 _layer_ptr(lse, "lse", torch.float32, (total_q, Hq), dev),
+                                 _layer_ptr(cu_q, "cu_q", torch.int32, (n + 1,), dev),
+                                 _layer_ptr(cu_k, "cu_k", torch.int32, (n + 1,), dev), n, total_q, total_k, Hq, Hkv, D,
+                                 1 if causal else 0, D ** -0.5 if scale is None else scale, _stream_handle(stream)))
+
+
+def attn_decode_workspace(B: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of the workspace of an attn_decode call (zeroed once before its first use)."""
+    n = int(lib().sgt_attn_decode_workspace_bytes(B, Hq, Hkv, D))
+    if n < 0:
+        _check(n)
+    return n
+
+
+def attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, workspace, *, lse=None, scale: Optional[float] = None,
+                stream=None):
+    """Attention of one new token per sequence over a paged cache (sgt_attn_decode).  q: B x Hq x D bf16, rows may be
+    strided; k_cache, v_cache: n_pages x page_size x Hkv x D bf16 with the same strides (a transposed view of
+    n_pages x Hkv x page_size x D can be passed); block_table: B x max_pages int32, rows may be strided; seq_lens: B
+    int32; out: B x Hq x D bf16 or fp32; workspace: at least attn_decode_workspace(B, Hq, Hkv, D) bytes."""
+    import torch
+    dev = _current_device(q, "q")
+    q_ptr, q_stride, q_head = _heads(q, "q", dev)
+    B, Hq, D = q.shape
+    if Hq > 1 and q_head != D:
+        raise ValueError("the heads of q must lie side by side")
+    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+        raise TypeError("the caches must be bfloat16, got %s and %s" % (k_cache.dtype, v_cache.dtype))
+    if k_cache.device != dev or v_cache.device != dev:
+        raise ValueError("the caches are on %s and %s, expected %s" % (k_cache.device, v_cache.device, dev))
+    st = k_cache.stride()
+    if len(st) != 4 or st[3] != 1 or v_cache.stride() != st or v_cache.shape != k_cache.shape or k_cache.shape[3] != D:
+        raise ValueError("k_cache and v_cache must be n_pages x page_size x Hkv x D with the same strides")
+    n_pages, page_size, Hkv = k_cache.shape[:3]
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or \
+            block_table.device != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be %d x max_pages int32 on %s with contiguous rows" % (B, dev))
+    max_pages = block_table.shape[1]
+    _check(lib().sgt_attn_decode(q_ptr, q_stride, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n_pages,
+                                 page_size, block_table.data_ptr(), block_table.stride(0) if B > 1 else max_pages,
+                                 max_pages, _layer_ptr(seq_lens, "seq_lens", torch.int32, (B,), dev),
+                                 _layer_ptr(out, "out", out.dtype, (B, Hq, D), dev), _dtype_code(out),
+                                 _layer_ptr(lse, "lse", torch.float32, (B, Hq), dev),
+                                 _dev_ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
+                                 B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _stream_handle(stream)))
 
 
 class Context:

@@ -1,0 +1,71 @@
+// Arguments of the transformer-layer operators' kernels (RMS norm, expert
+// gate, prompt attention, paged decode attention), filled by layer_api.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace sgt {
+
+struct NormArgs {
+  const void* x;         // T rows of H, x_stride elements apart
+  const void* residual;  // T x H, or null
+  const void* weight;    // H
+  void* sum_out;         // T x H, or null
+  void* out;             // T x H
+  float* scales;         // T x ceil(H / block) (block > 0) or T; 8-bit outputs only
+  int64_t T, x_stride;
+  int32_t H, block;
+  int32_t x_dtype, r_dtype, w_dtype, out_dtype;
+  float eps;
+};
+
+struct GateArgs {
+  const void* logits;  // T rows of E, stride elements apart
+  const float* bias;   // E, or null
+  int32_t* ids;        // T x k
+  float* gate;         // T x k
+  int64_t T, stride;
+  int32_t E, k;
+  int32_t n_group, topk_group, group_top;
+  int32_t sigmoid, renormalize, bf16;
+  float scale;
+};
+
+struct PromptArgs {
+  const uint16_t* q;    // total_q tokens of Hq x D; token and head strides in elements
+  const uint16_t* k;    // total_k tokens of Hkv x D
+  const uint16_t* v;
+  uint16_t* out;        // total_q x Hq x D, dense
+  float* lse;           // total_q x Hq, or null
+  const int32_t* cu_q;  // n_seqs + 1
+  const int32_t* cu_k;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  int64_t total_q, total_k;
+  int32_t n_seqs, Hq, Hkv, D, causal;
+  float scale;          // of the scores
+};
+
+struct DecodeArgs {
+  const uint16_t* q;       // B x Hq x D, q_stride elements between tokens
+  const uint16_t* k;       // cache: page, slot and head strides in elements
+  const uint16_t* v;
+  const int32_t* table;    // B rows of max_pages page ids, table_stride entries apart
+  const int32_t* lens;     // B
+  void* out;               // B x Hq x D bf16 or fp32
+  float* lse;              // B x Hq, or null
+  void* workspace;
+  int64_t q_stride, page_stride, slot_stride, head_stride, table_stride;
+  int64_t n_pages;
+  int32_t B, Hq, Hkv, D;
+  int32_t page_size, max_pages, out_f32;
+  float scale;
+};
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_moe_gate(const GateArgs& a, hipStream_t stream);
+hipError_t launch_attn_prompt(const PromptArgs& a, hipStream_t stream);
+hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t stream);
+int64_t attn_decode_workspace(int B, int Hq, int Hkv, int D);
+
+}  // namespace sgt

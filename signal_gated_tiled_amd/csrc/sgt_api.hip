@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "sgt.h"
+#include "api.hpp"
 #include "common.hpp"
 #include "ring.hpp"
 #include "sched.hpp"
@@ -64,6 +65,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace sgt {
+
 sgt_status fail(sgt_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -74,12 +79,9 @@ sgt_status fail(sgt_status st, const char* fmt, ...) {
   return st;
 }
 
-#define HIP_TRY(expr)                                                                            \
-  do {                                                                                           \
-    hipError_t e_ = (expr);                                                                      \
-    if (e_ != hipSuccess) return fail(SGT_EHIP, "%s: %s (%s:%d)", #expr, hipGetErrorString(e_), \
-                                      __FILE__, __LINE__);                                       \
-  } while (0)
+}  // namespace sgt
+
+namespace {
 
 constexpr int kSlots = 4;                 // producer schedule tables in flight
 // Counter words of a context: [0] GEMM+RS reduction claims, [32] AllGather

@@ -1,0 +1,572 @@
+"""The transformer-layer operators on the GPU against their fp64 definitions (oracle/layer.py).
+
+Tolerances, from the arithmetic the operators promise (fp32 inside, one rounding when stored; u = 2^-24):
+  * RMS norm: y is off by a few u from the sum of H squares (pairwise within lanes: below 16 u), the square root and
+    three products: 4e-6 |y| in fp32, plus the rounding 2^-9 |y| in bf16 and half a step of e4m3 (2^-4 |z|, or 2^-10
+    below the normal range) in 8 bits.  Scales: 4e-6 relative.
+  * Gate: exp of a difference of logits of up to 100 is off by 100 u plus a few u: 1e-5 relative.
+  * Attention: each weight exp(s - m) is rounded to bf16 once (2^-9) and its exponent is off by what 128 products
+    lose (below 2^-12 for the inputs here), so out is within 2^-8 sum_j p_j |v_j|, plus its own rounding 2^-8 |out| in
+    bf16.  lse does not see that rounding: 1e-5 (1 + |lse|), and the same relative to the largest score.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import signal_gated_tiled_amd as sgt  # noqa: E402
+from oracle import layer as L  # noqa: E402
+
+DEV = "cuda:0"
+NAN = float("nan")
+INF = float("inf")
+
+
+def rnd(rng, shape, dtype=torch.bfloat16, std=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * std).astype(np.float32)).to(dtype).to(DEV)
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def rows(t, pad):
+    """The same matrix with `pad` more elements between its rows."""
+    wide = torch.full((t.shape[0], t.shape[1] + pad), NAN, dtype=t.dtype, device=t.device)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+def near(got, ref, rel, floor=0.0, extra=0.0):
+    got = f64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == ref.shape
+    bad = ~(np.abs(got - ref) <= rel * np.abs(ref) + floor + extra) & ~(np.isnan(ref) & np.isnan(got)) & ~(got == ref)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3].tolist(), got[bad][:3], ref[bad][:3])
+
+
+# ------------------------------------------------------------------ RMS norm
+
+WIDTHS = [1, 7, 64, 100, 128, 129, 1000, 1024, 2048, 2056, 4099, 5120, 8192, 16384, 16392, 40000, 65536]
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("x_dtype", [torch.bfloat16, torch.float32])
+def test_norm_widths(H, x_dtype):
+    rng = np.random.default_rng(H)
+    T = 5 if H < 20000 else 2
+    x, r, w = rnd(rng, (T, H), x_dtype), rnd(rng, (T, H)), rnd(rng, (H,))
+    s_ref, y_ref = L.rms_norm(f64(x), f64(r), f64(w), 1e-6)
+    s, y = torch.empty_like(r), torch.empty_like(r)
+    sgt.rms_norm(x, w, y, residual=r, sum_out=s)
+    near(s, s_ref, 2.0 ** -8, 1e-30)
+    near(y, y_ref, 2.0 ** -8, 1e-6)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 255, 1025])
+@pytest.mark.parametrize("H", [96, 2048, 5120])
+@pytest.mark.parametrize("block", [0, 128])
+def test_norm_8bit(T, H, block):
+    rng = np.random.default_rng(T + H)
+    x, r, w = rnd(rng, (T, H), torch.float32, 0.3), rnd(rng, (T, H)), rnd(rng, (H,), torch.float32)
+    _, y_ref = L.rms_norm(f64(x), f64(r), f64(w), 1e-5)
+    scales_ref = L.f8_scales(y_ref, block)
+    out = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=DEV)
+    scales = torch.empty(scales_ref.shape, device=DEV)
+    sgt.rms_norm(x, w, out, residual=r, scales=scales, eps=1e-5)
+    near(scales, scales_ref, 4e-6)
+    z = y_ref / np.repeat(scales_ref, block or H, axis=1)[:, :H]
+    near(out, z, 2.0 ** -4 + 1e-5, 2.0 ** -10 + 1e-5)
+    assert float(out.float().abs().max()) == 448.0
+
+
+@pytest.mark.parametrize("H", [130, 2048, 5120])
+@pytest.mark.parametrize("x_dtype,r_dtype,w_dtype,out_dtype", [
+    (torch.float32, torch.float32, torch.float32, torch.float32), (torch.bfloat16, torch.float32, torch.bfloat16, torch.float32),
+    (torch.float32, torch.bfloat16, torch.float32, torch.bfloat16), (torch.bfloat16, torch.bfloat16, torch.float32, torch.bfloat16)])
+def test_norm_types_and_strides(H, x_dtype, r_dtype, w_dtype, out_dtype):
+    rng = np.random.default_rng(H)
+    x, r, w = rows(rnd(rng, (9, H), x_dtype), 3), rnd(rng, (9, H), r_dtype), rnd(rng, (H,), w_dtype)
+    s_ref, y_ref = L.rms_norm(f64(x), f64(r), f64(w), 1e-6)
+    s, y = torch.empty_like(r), torch.empty(9, H, dtype=out_dtype, device=DEV)
+    sgt.rms_norm(x, w, y, residual=r, sum_out=s)
+    near(s, s_ref, 2e-7 if r_dtype == torch.float32 else 2.0 ** -8)
+    near(y, y_ref, 4e-6 if out_dtype == torch.float32 else 2.0 ** -8, 1e-6)
+    # without a residual, without a sum; rows of any alignment
+    flat = torch.zeros(9 * H + 1, dtype=x_dtype, device=DEV)
+    x1 = flat[1:].view(9, H)
+    x1.copy_(x)
+    sgt.rms_norm(x1, w, y)
+    near(y, L.rms_norm(f64(x), None, f64(w), 1e-6)[1], 4e-6 if out_dtype == torch.float32 else 2.0 ** -8, 1e-6)
+
+
+def test_norm_in_place():
+    rng = np.random.default_rng(1)
+    for H in (131, 5120, 20000):
+        x, r, w = rnd(rng, (6, H)), rnd(rng, (6, H)), rnd(rng, (H,))
+        s_ref, y_ref = L.rms_norm(f64(x), f64(r), f64(w), 1e-6)
+        sgt.rms_norm(x, w, x, residual=r, sum_out=r)
+        near(r, s_ref, 2.0 ** -8)
+        near(x, y_ref, 2.0 ** -8, 1e-6)
+
+
+def test_norm_zero_rows_nan_rows_and_extremes():
+    H = 2048
+    x = torch.zeros(5, H, device=DEV)
+    x[1, 7] = NAN
+    x[2, 9] = INF
+    x[3] = 1e15        # the square overflows bf16's neighbours, not fp32
+    x[4] = 1e-20
+    w = torch.ones(H, device=DEV)
+    y = torch.empty(5, H, device=DEV)
+    sgt.rms_norm(x, w, y, eps=1e-6)
+    assert (y[0] == 0).all() and torch.isnan(y[1]).all()
+    assert torch.isnan(y[2, 9]) and (y[2, :9] == 0).all()
+    assert torch.allclose(y[3], torch.ones_like(y[3])) and torch.allclose(y[4], x[4] * 1e3)
+    out = torch.empty(5, H, dtype=torch.float8_e4m3fn, device=DEV)
+    for n in (1, 16):
+        scales = torch.empty(5, n, device=DEV)
+        sgt.rms_norm(x, w, out, scales=scales, eps=1e-6)
+        assert (scales[0] == 2.0 ** -126).all() and (out[0].float() == 0).all()
+        assert torch.isnan(out[1].float()).all() and torch.isnan(scales[1]).all()
+        assert (out[3].float() == 448).all()
+
+
+def test_norm_many_rows_past_32_bits():
+    H, T = 8192, 262144 + 3   # 2^31 elements and more
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    rng = np.random.default_rng(2)
+    at = [0, 1, T // 2, T - 2, T - 1]
+    vals = rnd(rng, (len(at), H))
+    x[at] = vals
+    w = rnd(rng, (H,))
+    sgt.rms_norm(x, w, x)
+    near(x[at], L.rms_norm(f64(vals), None, f64(w), 1e-6)[1], 2.0 ** -8, 1e-6)
+
+
+# ------------------------------------------------------------------ gate
+
+def check_gate(x, k, **kw):
+    T = x.shape[0]
+    ids, gate = torch.full((T, k), -7, dtype=torch.int32, device=DEV), torch.full((T, k), NAN, device=DEV)
+    sgt.moe_gate(x, ids, gate, **kw)
+    if "bias" in kw and kw["bias"] is not None:
+        kw = dict(kw, bias=f64(kw["bias"]))
+    if kw.get("n_group", 1) > 1:
+        kw = dict({"group_top": 2}, **kw)
+    ref_ids, ref = L.moe_gate(f64(x), k, **kw)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
+    near(gate, ref, 1e-5, 1e-30)
+
+
+def grid(rng, shape, step, lo, hi, dtype=torch.float32):
+    """Logits on a grid: two are equal or clearly apart, so that every way to round orders them alike."""
+    return torch.from_numpy((rng.integers(lo, hi, shape) * step).astype(np.float32)).to(dtype).to(DEV)
+
+
+@pytest.mark.parametrize("T", [1, 3, 64, 1001])
+@pytest.mark.parametrize("E,k", [(1, 1), (5, 5), (16, 4), (60, 6), (64, 8), (65, 8), (128, 2), (160, 6), (256, 8), (512, 10),
+                                 (1000, 64), (1024, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_shapes(T, E, k, score):
+    if T == 1001 and E > 256:
+        T = 65
+    rng = np.random.default_rng(T + E)
+    check_gate(grid(rng, (T, E), 2.0 ** -6, -300, 300), k, score=score, renormalize=k > 1)
+
+
+def clearly_apart(x, bias, score, g, top):
+    """The tokens whose choice hangs on no difference below 1e-6, which fp32 and fp64 could order differently."""
+    z = f64(x)
+    e = np.exp(z - z.max(1, keepdims=True))
+    c = (e / e.sum(1, keepdims=True) if score == "softmax" else 1 / (1 + np.exp(-z))) + f64(bias)
+    by = np.sort(np.sort(c.reshape(len(z), g, -1), axis=2)[:, :, -top:].sum(2), axis=1)
+    ok = (np.diff(np.sort(c, axis=1), axis=1)[:, -64:] > 1e-6).all(1) & (np.diff(by, axis=1) > 1e-6).all(1)
+    assert ok.sum() >= 10
+    return x[torch.from_numpy(ok).to(x.device)].contiguous()
+
+
+@pytest.mark.parametrize("E,g,kept,k", [(64, 8, 3, 6), (256, 8, 4, 8), (256, 64, 9, 8), (160, 8, 3, 6), (72, 4, 2, 5),
+                                        (1024, 16, 5, 32), (30, 3, 1, 10), (128, 32, 4, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2])
+def test_gate_groups_and_bias(E, g, kept, k, score, top):
+    rng = np.random.default_rng(E + g)
+    x = grid(rng, (37, E), 2.0 ** -6, -300, 300)
+    bias = torch.from_numpy(rng.standard_normal(E).astype(np.float32)).to(DEV)
+    check_gate(clearly_apart(x, bias, score, g, top), k, score=score, bias=bias, n_group=g, topk_group=kept, group_top=top, scale=2.5)
+    check_gate(x, k, score=score, n_group=g, topk_group=kept, group_top=1, renormalize=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gate_types_strides_and_ties(dtype):
+    rng = np.random.default_rng(3)
+    check_gate(rows(grid(rng, (33, 96), 0.125, -20, 20, dtype), 5), 7)
+    check_gate(torch.zeros(5, 64, dtype=dtype, device=DEV), 8)                      # all equal: ids 0..7
+    check_gate(torch.zeros(5, 256, dtype=dtype, device=DEV), 8, score="sigmoid", n_group=8, topk_group=2, group_top=1)
+    check_gate(torch.zeros(5, 64, device=DEV), 4, score="sigmoid", bias=torch.ones(64, device=DEV))
+
+
+def test_gate_infinities_and_nan():
+    x = torch.zeros(8, 64, device=DEV)
+    x[0, 3:] = -INF                      # three experts left of a padded table
+    x[1] = -INF                          # none
+    x[2, 5] = NAN
+    x[3] = NAN
+    x[4, 9] = INF
+    x[5, 9] = x[5, 40] = INF
+    x[6] = torch.linspace(-200, 200, 64)
+    x[7, ::2] = -3.4e38                  # the type's lowest value as a mask
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            check_gate(x, 8, score=score, renormalize=renorm)
+    bias = torch.arange(64, device=DEV) * 0.0625
+    bias[60] = -INF
+    bias[3] = NAN
+    check_gate(x[:1], 8, score="sigmoid", bias=bias)
+    check_gate(x[4:5], 8, score="sigmoid", bias=bias)
+
+
+# ------------------------------------------------------------------ attention over prompts
+
+def make_prompt(rng, nq, nk, hq, hkv, d, fused=False, std=1.0):
+    tq, tk = sum(nq), sum(nk)
+    if fused:
+        qkv = rnd(rng, (tq, hq + 2 * hkv, d), std=std)
+        return qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    return rnd(rng, (tq, hq, d), std=std), rnd(rng, (tk, hkv, d), std=std), rnd(rng, (tk, hkv, d))
+
+
+def cu(n):
+    return torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device=DEV)
+
+
+def check_attention(out, lse, ref, out_f32=False):
+    o, z, mag = ref
+    near(out, o, 0.0 if out_f32 else 2.0 ** -8, 1e-6, 2.0 ** -8 * mag)
+    finite = np.isfinite(z)
+    got = f64(lse)
+    assert np.array_equal(np.isfinite(got), finite) and (got[~finite] == -INF).all()
+    near(got[finite], z[finite], 1e-5, 1e-5)
+
+
+def check_prompt(q, k, v, nq, nk, causal=True, scale=None):
+    tq, hq, d = q.shape
+    out, lse = torch.full((tq, hq, d), NAN, dtype=torch.bfloat16, device=DEV), torch.full((tq, hq), NAN, device=DEV)
+    sgt.attn_prompt(q, k, v, out, cu(nq), cu(nk), lse=lse, causal=causal, scale=scale)
+    cq, ck = np.concatenate([[0], np.cumsum(nq)]), np.concatenate([[0], np.cumsum(nk)])
+    check_attention(out, lse, L.packed_attention(f64(q), f64(k), f64(v), cq, ck, d ** -0.5 if scale is None else scale, causal))
+    return out, lse
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 31, 32, 33, 63, 64, 65, 127, 129, 255, 257, 500])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1), (6, 2)])
+def test_prompt_lengths(n, d, hq, hkv):
+    rng = np.random.default_rng(n + d)
+    q, k, v = make_prompt(rng, [n], [n], hq, hkv, d, fused=True)
+    check_prompt(q, k, v, [n], [n])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (5, 1), (16, 2), (40, 1)])
+def test_prompt_packed(d, causal, hq, hkv):
+    rng = np.random.default_rng(d + hq)
+    n = [3, 0, 130, 1, 64, 65, 0, 200, 2]
+    q, k, v = make_prompt(rng, n, n, hq, hkv, d, fused=True)
+    check_prompt(q, k, v, n, n, causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk", [([5], [1000]), ([1, 1, 1], [70, 1, 300]), ([100, 7], [611, 7]), ([64, 0, 33], [128, 9, 640]),
+                                   ([20, 300], [7, 100]), ([3, 4], [0, 5]), ([300], [1])])
+def test_prompt_pieces_and_empty_rows(nq, nk, causal):
+    """Queries after a computed prefix; queries that come before the first key and see nothing."""
+    rng = np.random.default_rng(sum(nq))
+    for hq, hkv, d in ((8, 2, 128), (3, 3, 64)):
+        q, k, v = make_prompt(rng, nq, nk, hq, hkv, d)
+        check_prompt(q, k, v, nq, nk, causal)
+
+
+def test_prompt_large_scores_and_scale():
+    rng = np.random.default_rng(4)
+    n = [150, 90]
+    q, k, v = make_prompt(rng, n, n, 4, 2, 128, std=4.0)
+    check_prompt(q, k, v, n, n)
+    check_prompt(q, k, v, n, n, scale=0.0)
+    check_prompt(q, k, v, n, n, scale=-0.05)
+    # the maximum rises along the keys, block after block
+    k = (torch.linspace(-6, 6, 240, device=DEV)[:, None, None] * q[:1, :2].float().sign()).to(torch.bfloat16).contiguous()
+    check_prompt(q, k, v, n, n)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_unseen_values_do_not_reach_the_output(bad, d):
+    rng = np.random.default_rng(5)
+    n = [70, 200]
+    q, k, v = make_prompt(rng, n, n, 4, 2, d)
+    clean, clean_lse = check_prompt(q, k, v, n, n)
+    for token in (40, 69, 70 + 33, 70 + 130, 269):
+        k2, v2 = k.clone(), v.clone()
+        k2[token], v2[token] = bad, bad
+        out, lse = torch.empty_like(clean), torch.empty_like(clean_lse)
+        sgt.attn_prompt(q, k2, v2, out, cu(n), cu(n), lse=lse)
+        sees = np.zeros(270, bool)
+        sees[token:70 if token < 70 else 270] = True
+        ok = torch.from_numpy(~sees).to(DEV)
+        assert torch.equal(out[ok], clean[ok]) and torch.equal(lse[ok], clean_lse[ok])
+        if bad != bad:
+            assert torch.isnan(out[~ok].float()).all()
+
+
+def test_prompt_value_infinities_reach_those_that_see_them():
+    rng = np.random.default_rng(6)
+    q, k, v = make_prompt(rng, [100], [100], 2, 1, 64)
+    v[50, 0, 3], v[60, 0, 4] = INF, NAN
+    out = torch.empty_like(q)
+    sgt.attn_prompt(q, k, v, out, cu([100]), cu([100]))
+    o = out.float()
+    assert (o[50:, :, 3] == INF).all() and torch.isfinite(o[:50]).all()
+    assert torch.isnan(o[60:, :, 4]).all() and torch.isfinite(o[:60, :, 4]).all()
+    assert torch.isfinite(o[:, :, 5:]).all()
+
+
+def test_prompt_strides_and_rows_outside():
+    rng = np.random.default_rng(7)
+    wide = rnd(rng, (120, 24, 128))
+    q, k, v = wide[:, 2:10], wide[:, 12:16:2], wide[:, 13:17:2]     # heads that lie apart
+    check_prompt(q, k, v, [50, 70], [50, 70])
+    heads_first = rnd(rng, (4, 90, 64)).transpose(0, 1)
+    check_prompt(heads_first, heads_first[:, :2], heads_first[:, 2:], [90], [90])
+    # offsets that leave rows out, or point outside: nothing else is written, nothing outside is read
+    out = torch.full((120, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([10, 40, 500], dtype=torch.int32, device=DEV)
+    sgt.attn_prompt(q, k, v, out, off, off)
+    assert (out[:10] == 7).all() and torch.isfinite(out.float()).all() and not (out[10:] == 7).all(2).all(1).any()
+    ref = torch.empty_like(out[10:40])
+    sgt.attn_prompt(q[10:40], k[10:40], v[10:40], ref, cu([30]), cu([30]))
+    assert torch.equal(out[10:40], ref)
+
+
+def test_prompt_many_sequences():
+    rng = np.random.default_rng(8)
+    n = list(rng.integers(0, 9, 700))
+    q, k, v = make_prompt(rng, n, n, 2, 1, 64, fused=True)
+    check_prompt(q, k, v, n, n)
+
+
+def test_prompt_long_is_the_sum_of_its_halves():
+    """A length at which fp64 loops take too long: the lse and out of 9000 keys against both halves' joined."""
+    rng = np.random.default_rng(9)
+    q, k, v = make_prompt(rng, [64], [9000], 8, 1, 128)
+    parts = []
+    for a, b in ((0, 9000), (0, 4100), (4100, 9000)):
+        out, lse = torch.empty_like(q), torch.empty(64, 8, device=DEV)
+        sgt.attn_prompt(q, k[a:b], v[a:b], out, cu([64]), cu([b - a]), lse=lse, causal=False)
+        parts.append((f64(out), f64(lse)))
+    (o, z), (o1, z1), (o2, z2) = parts
+    joined = np.logaddexp(z1, z2)
+    near(z, joined, 1e-5, 1e-5)
+    near(o, np.exp(z1 - joined)[..., None] * o1 + np.exp(z2 - joined)[..., None] * o2, 2.0 ** -6, 2.0 ** -6 * np.abs(o).max())
+
+
+# ------------------------------------------------------------------ decode
+
+def make_cache(rng, lens, page, hkv, d, order="slot", spare=2, width=None, fill=None):
+    count = [-(-int(n) // page) for n in lens]
+    pages = sum(count) + spare
+    shape = (pages, page, hkv, d) if order == "slot" else (pages, hkv, page, d)
+    k, v = rnd(rng, shape), rnd(rng, shape)
+    if order == "head":
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+    perm = rng.permutation(pages)
+    table = np.full((len(lens), width or max(max(count), 1)), -1, np.int32)
+    at = 0
+    for b, c in enumerate(count):
+        table[b, :c] = perm[at:at + c]
+        at += c
+    if fill is not None:   # every slot that holds no token
+        seen = np.zeros((pages, page), bool)
+        for b, n in enumerate(lens):
+            for j in range(int(n)):
+                seen[table[b, j // page], j % page] = True
+        free = torch.from_numpy(~seen).to(DEV)
+        k[free], v[free] = fill, fill
+    return k, v, torch.from_numpy(table).to(DEV), torch.tensor(np.array(lens), dtype=torch.int32, device=DEV)
+
+
+def workspace(B, hq, hkv, d):
+    return torch.zeros(sgt.attn_decode_workspace(B, hq, hkv, d), dtype=torch.uint8, device=DEV)
+
+
+def check_decode(rng, q, k, v, table, lens, out_dtype=torch.bfloat16, ref=None, scale=None):
+    B, hq, d = q.shape
+    ws = workspace(B, hq, k.shape[2], d)
+    if ref is None:
+        ref = L.paged_attention(f64(q), f64(k), f64(v), table.cpu().numpy(), lens.cpu().numpy(),
+                                d ** -0.5 if scale is None else scale)
+    first = None
+    for _ in range(2):   # the workspace is ready for the next call, and the bits are the same
+        out, lse = torch.full((B, hq, d), NAN, dtype=out_dtype, device=DEV), torch.full((B, hq), NAN, device=DEV)
+        sgt.attn_decode(q, k, v, table, lens, out, ws, lse=lse, scale=scale)
+        check_attention(out, lse, ref, out_dtype == torch.float32)
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    return first
+
+
+@pytest.mark.parametrize("page", [1, 7, 16, 64, 100])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1), (6, 2), (16, 1), (20, 1), (32, 4), (64, 1)])
+def test_decode_layouts(page, d, hq, hkv):
+    rng = np.random.default_rng(page + d + hq)
+    lens = [1, 0, 15, 16, 17, 100, 333, 64]
+    k, v, table, n = make_cache(rng, lens, page, hkv, d, "slot" if page % 2 else "head", fill=NAN)
+    check_decode(rng, rnd(rng, (len(lens), hq, d)), k, v, table, n,
+                 out_dtype=torch.float32 if d == 64 else torch.bfloat16)
+
+
+@pytest.mark.parametrize("lens", [[0], [1], [31], [32], [33], [2049], [5000, 3], [0, 0, 0], [700] * 40, [1] * 300])
+def test_decode_lengths(lens):
+    rng = np.random.default_rng(len(lens) + lens[0])
+    k, v, table, n = make_cache(rng, lens, 16, 2, 128, fill=INF)
+    check_decode(rng, rnd(rng, (len(lens), 8, 128)), k, v, table, n)
+
+
+def test_decode_long_cache():
+    rng = np.random.default_rng(11)
+    lens = [40000, 9, 17000]
+    k, v, table, n = make_cache(rng, lens, 32, 1, 64)
+    check_decode(rng, rnd(rng, (3, 4, 64), std=2.0), k, v, table, n)
+
+
+def test_decode_lengths_and_pages_outside():
+    rng = np.random.default_rng(12)
+    k, v, table, n = make_cache(rng, [100, 100, 100, 100], 16, 1, 128, width=7)
+    n[0], n[1] = 1000, -5            # more than the table holds; less than nothing
+    table[0, 2], table[2, 3], table[3, :] = 10 ** 9, -1, -1
+    out, lse = check_decode(rng, rnd(rng, (4, 8, 128)), k, v, table, n)
+    assert (out[1] == 0).all() and (lse[3] == -INF).all() and (out[3] == 0).all()
+
+
+def test_decode_strided_queries_and_table():
+    rng = np.random.default_rng(13)
+    k, v, table, n = make_cache(rng, [50, 60, 70], 16, 2, 64)
+    wide = rnd(rng, (3, 12, 64))
+    tw = torch.full((3, 40), 10 ** 6, dtype=torch.int32, device=DEV)
+    tw[:, :table.shape[1]] = table
+    check_decode(rng, wide[:, 2:10], k, v, tw[:, :table.shape[1]], n)
+    check_decode(rng, wide[:, 2:10], k, v, table, n, scale=0.7)
+
+
+def test_decode_large_scores():
+    rng = np.random.default_rng(14)
+    k, v, table, n = make_cache(rng, [3000, 40], 16, 1, 128)
+    check_decode(rng, rnd(rng, (2, 8, 128), std=12.0), k, v, table, n)
+
+
+def test_decode_cache_past_32_bits():
+    """Pages more than 2^31 elements (and 2^32 bytes) apart."""
+    rng = np.random.default_rng(15)
+    page, hkv, d = 64, 8, 128
+    pages = (1 << 31) // (page * hkv * d) + 40
+    k = torch.zeros(pages, page, hkv, d, dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros_like(k)
+    use = [pages - 1, 3, pages - 20, pages // 2]
+    for p in use:
+        k[p], v[p] = rnd(rng, (page, hkv, d)), rnd(rng, (page, hkv, d))
+    table = torch.tensor([use], dtype=torch.int32, device=DEV)
+    n = torch.tensor([250], dtype=torch.int32, device=DEV)
+    q = rnd(rng, (1, 16, d))
+    small_k, small_v = torch.stack([k[p] for p in use]), torch.stack([v[p] for p in use])
+    ref = L.paged_attention(f64(q), f64(small_k), f64(small_v), np.arange(4)[None], [250], d ** -0.5)
+    check_decode(rng, q, k, v, table, n, ref=ref)
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def layer_calls(rng):
+    """One call of each operator on fixed buffers: (function, outputs)."""
+    x, r, w = rnd(rng, (50, 2048)), rnd(rng, (50, 2048)), rnd(rng, (2048,))
+    y, s = torch.empty_like(x), torch.empty_like(x)
+    logits = grid(rng, (50, 64), 2.0 ** -6, -300, 300)
+    ids, gate = torch.empty(50, 8, dtype=torch.int32, device=DEV), torch.empty(50, 8, device=DEV)
+    q, k, v = make_prompt(rng, [300], [300], 8, 2, 128)
+    out = torch.empty_like(q)
+    off = cu([300])
+    kc, vc, table, n = make_cache(rng, [2000, 5, 700], 16, 2, 128)
+    q1 = rnd(rng, (3, 8, 128))
+    o1 = torch.empty_like(q1)
+    ws = workspace(3, 8, 2, 128)
+
+    def run(stream=None):
+        sgt.rms_norm(x, w, y, residual=r, sum_out=s, stream=stream)
+        sgt.moe_gate(logits, ids, gate, stream=stream)
+        sgt.attn_prompt(q, k, v, out, off, off, stream=stream)
+        sgt.attn_decode(q1, kc, vc, table, n, o1, ws, stream=stream)
+    return run, (y, s, ids, gate, out, o1)
+
+
+def test_side_stream_gives_the_same():
+    run, outs = layer_calls(np.random.default_rng(20))
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    for t in outs:
+        t.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    run(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_graph_replays_give_the_same():
+    run, outs = layer_calls(np.random.default_rng(21))
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(4):
+        for t in outs:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        run()                                # eager work between the replays
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_binding_refuses_wrong_tensors():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    w = x[0]
+    with pytest.raises(ValueError, match="shape"):
+        sgt.rms_norm(x, w[:32], x)
+    with pytest.raises(ValueError, match="scales"):
+        sgt.rms_norm(x, w, torch.zeros(4, 64, dtype=torch.float8_e4m3fn, device=DEV))
+    with pytest.raises(TypeError):
+        sgt.rms_norm(x.half(), w, x)
+    ids = torch.zeros(4, 8, dtype=torch.int32, device=DEV)
+    with pytest.raises(TypeError, match="topk_ids"):
+        sgt.moe_gate(x, ids.long(), ids.float())
+    with pytest.raises(sgt.SgtError, match="topk"):
+        sgt.moe_gate(x[:, :4], ids, ids.float())
+    q = x.view(4, 1, 64)
+    with pytest.raises(TypeError, match="bfloat16"):
+        sgt.attn_prompt(q.float(), q, q, q, cu([4]), cu([4]))
+    with pytest.raises(ValueError, match="cu_k"):
+        sgt.attn_prompt(q, q, q, torch.empty_like(q), cu([4]), cu([2, 2]))
+    with pytest.raises(ValueError, match="same strides"):
+        sgt.attn_decode(q, q[None], q[None].transpose(1, 2), ids, ids[:, 0].contiguous(), q, x)
+    cache = torch.zeros(2, 16, 1, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(sgt.SgtError, match="workspace"):
+        sgt.attn_decode(q, cache, cache, ids, torch.zeros(4, dtype=torch.int32, device=DEV), torch.empty_like(q),
+                        torch.zeros(0, dtype=torch.uint8, device=DEV))
