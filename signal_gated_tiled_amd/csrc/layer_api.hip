@@ -114,7 +114,8 @@ sgt_status sgt_attn_prompt(const void* q, int64_t q_token, int64_t q_head, const
     return fail(SGT_EUNSUPPORTED, "a token stride of 2^24 elements or more");
   if (total_q == 0) return SGT_OK;
   if (n_seqs == 0) return fail(SGT_EINVAL, "total_q = %lld tokens in no sequence", (long long)total_q);
-  if (total_q * Hq / 16 + n_seqs >= kMaxRows / Hkv) return fail(SGT_EINVAL, "too many rows for one launch");
+  if (total_q * (Hq / Hkv) > kMaxRows || total_q * Hq / 32 + (int64_t)n_seqs * Hkv > kMaxRows)
+    return fail(SGT_EINVAL, "too many rows (tokens x heads) for one launch");
   if (!q || !out || !cu_q || !cu_k || (total_k > 0 && (!k || !v)))
     return fail(SGT_EINVAL, "q, k, v, out, cu_q or cu_k is NULL");
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
