@@ -1,65 +1,505 @@
 // Attention of one new token per sequence over a paged key-value cache.
+//
+// The cache's bytes bound this: each key and value is read once for the up to
+// 16 kNQ query heads that share it, on the matrix cores (the heads as columns), so
+// that the arithmetic stays far below the memory's time.
+//
+// Split and join.  The work is a list of problems (sequence, key head, chunk of
+// query heads), each a row of tiles of 2 KiB / D keys; the tiles of all problems,
+// one after another, are cut into equal ranges, one per workgroup, whatever the
+// lengths.  A workgroup that holds all of a problem's tiles writes the result; else
+// it writes its part (unnormalised output, maximum, sum) to the workspace and counts
+// itself in, and the last one to do so joins the parts in their order, so the
+// bits do not depend on who came last.
+//
+// Inside a workgroup the four waves take every fourth tile each, without
+// barriers: each wave has a ring of four LDS stages of its own, filled by
+// HBM-to-LDS DMA three tiles ahead (24 KiB in flight per wave, 96 KiB per CU), and
+// page ids are loaded four tiles ahead of that.  Loads return in order, so waiting
+// until no more than the two younger tiles' loads are left is waiting for the tile;
+// past its last tile a wave loads that one again, which keeps the count.
+//
+// Running maximum and sum as in the prompt kernel: S^T = K Q^T leaves one query
+// head per lane column, its registers are the B operand of O^T += V^T P^T, V^T comes
+// from the transposing LDS read, and the maximum moves only when a weight would
+// pass 2^8.
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
 #include "layer.hpp"
+#include "mfma_tile.hpp"
+#include "signal.hpp"
 
 namespace sgt {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kRing = 4;                      // LDS stages of a wave
+constexpr int kGrid = 256;                   // workgroups: one on each CU (128 KiB of LDS)
+constexpr int kMinTiles = 4;                 // tiles of a range at least: one for each wave
+constexpr int kMaxParts = 64;                // a problem is cut into about this many parts at most
+constexpr int kMaxRows = 32;                 // query heads of a chunk
+constexpr int kSlotFloats = kMaxRows * 128 + 2 * kMaxRows;   // one part: outputs, maxima, sums
+constexpr float kSlack = 8.f;                // log2 of the largest weight before the maximum moves
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// One wave per (sequence, query head), the head's dimensions over the lanes.
-template <int kD>
-__global__ void __launch_bounds__(64 * kWaves) attn_decode_kernel(DecodeArgs a) {
-  constexpr int kPer = kD / 64;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int item = blockIdx.x * kWaves + wv;
-  const int b = item / a.Hq, h = item % a.Hq;
-  if (b >= a.B) return;
-  const int hk = h / (a.Hq / a.Hkv);
-  const int64_t room = (int64_t)a.max_pages * a.page_size;
-  const int n = (int)min((int64_t)max(a.lens[b], 0), room);
-  float q[kPer], acc[kPer] = {};
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_ptr;
+typedef const __attribute__((address_space(1))) uint8_t* gptr_t;
+typedef const __attribute__((address_space(1))) void* gvoid_t;
+
+template <int kD> __host__ __device__ constexpr int tile_keys() { return 2048 / kD; }
+
+// 16-byte chunk c of row r is stored at chunk c ^ swizzle(r): the 16 rows of a key read (one chunk each) and of a
+// transposing value read (32 bytes each) then spread over all banks.
+template <int kD> __device__ __forceinline__ int k_swz(int row) { return kD == 128 ? (row & 15) : ((row >> 1) & 7); }
+template <int kD> __device__ __forceinline__ int v_swz(int row) {
+  return kD == 128 ? (row & 7) << 1 : ((row >> 1) & 3) << 1;
+}
+
+template <int kT>
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int64_t room) {
+  if (b >= a.B) return 0;
+  const int64_t n = min((int64_t)max(a.lens[b], 0), room);
+  return (int)max((n + kT - 1) / kT, (int64_t)1);   // an empty sequence is one tile of unseen keys
+}
+
+// A value that all lanes share, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v);
+  return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | lo);
+}
+
+// Inclusive prefix sum over the workgroup and its total; `red` holds kWaves words.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) q[i] = bf16_to_f32(a.q[b * a.q_stride + h * kD + lane + 64 * i]);
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n; ++j) {
-    const int64_t page = a.table[b * a.table_stride + j / a.page_size];
-    if (page < 0 || page >= a.n_pages) continue;
-    const int64_t at = page * a.page_stride + (j % a.page_size) * a.slot_stride + hk * a.head_stride + lane;
-    float z = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) z += q[i] * bf16_to_f32(a.k[at + 64 * i]);
-    z = wave_sum(z) * a.scale;
-    const float mn = fmaxf(m, z);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float r = expf(m - base), p = expf(z - base);
-    l = l * r + p;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * r + p * bf16_to_f32(a.v[at + 64 * i]);
-    m = mn;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t u = __shfl_up(v, o);
+    if (lane >= o) v += u;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int dt = a.out_f32 ? SGT_F32 : SGT_BF16;
+  __syncthreads();
+  if (lane == 63) red[w] = v;
+  __syncthreads();
+  int64_t all = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    store_elem(a.out, dt, ((int64_t)b * a.Hq + h) * kD + lane + 64 * i, l == 0.f ? 0.f : acc[i] * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)b * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < w) v += red[i];
+    all += red[i];
+  }
+  *total = all;
+  return v;
+}
+
+// Wait until at most n vector memory operations are outstanding.
+// (the builtin, so that the compiler counts with it; the operand's other counters are left alone).
+template <int n> __device__ __forceinline__ void wait_vm() {
+  static_assert(n < 64, "vmcnt has 6 bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+
+// The lane's number, hidden from the optimiser: what is computed from it stays where it is used (rare paths, or one
+// xor per use) instead of filling registers across the loop.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+template <int kD, int kNQ>
+__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, int chunks, float* parts, uint32_t* counters) {
+  constexpr int kT = tile_keys<kD>();              // keys per tile
+  constexpr int kTile = kT * kD * 2;               // bytes of a tile of keys or values: 4 KiB
+  constexpr int kDma = kTile / 1024;               // 1 KiB DMA loads of each
+  constexpr int kRowChunks = kD / 8, kDmaRows = 64 / kRowChunks;
+  constexpr int kGroup = 64 / kT, kPages = kRing / kGroup;   // tiles whose rows one register of page ids covers
+  constexpr int kQ = 16 * kNQ;                     // query heads of a chunk
+  constexpr int kS = kT / 16;                      // 16-key blocks of a tile
+  constexpr int kNB = kD / 16;                     // 16-column blocks of the output
+  struct Stage { uint8_t k[kTile], v[kTile]; };
+  // distinct objects, so that the compiler knows that a DMA into one is not read through another
+  __shared__ __attribute__((aligned(1024))) Stage sA[kWaves], sB[kWaves], sC[kWaves], sD[kWaves];
+  __shared__ int64_t sRow[kWaves][64];             // byte offsets in the cache of the rows of kGroup tiles
+  __shared__ float sM[kWaves][kMaxRows], sL[kWaves][kMaxRows];
+  __shared__ int64_t red[kWaves], found[2];
+  __shared__ int last;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), g = lane >> 4, col = lane & 15;
+  const int G = a.Hq / a.Hkv, HC = a.Hkv * chunks;
+  const int64_t room = (int64_t)a.max_pages * a.page_size;
+
+  // this workgroup's range of the units (tiles of all problems in order)
+  int64_t total = 0;
+  int top = 0;
+  for (int c = 0; c < a.B; c += kThreads) {
+    const int n = tiles_of<kT>(a, c + tid, room);
+    int64_t t;
+    block_scan(n, red, &t);
+    total += t;
+    top = max(top, n);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
+  __syncthreads();
+  if (lane == 0) red[w] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) top = max(top, (int)red[i]);
+  top = uniform(top);
+  const int64_t units = uniform(total) * HC;
+  const int64_t grid = gridDim.x;
+  const int64_t chunk = max(max((units + grid - 1) / grid, (int64_t)kMinTiles), (int64_t)(top + kMaxParts - 1) / kMaxParts);
+  const int64_t u0 = blockIdx.x * chunk, u1 = min(u0 + chunk, units);
+  if (u0 >= units) return;
+  for (int64_t c = 0, before = 0; c < a.B; c += kThreads) {
+    const int n = tiles_of<kT>(a, (int)c + tid, room);
+    int64_t t;
+    const int64_t end = before + block_scan(n, red, &t);
+    if (n > 0 && (end - n) * HC <= u0 && u0 < end * HC) {
+      found[0] = c + tid;
+      found[1] = end - n;
+    }
+    before += t;
+    if (before * HC > u0) break;
+  }
+  __syncthreads();
+  int b = uniform((int)found[0]);
+  int64_t start = uniform(found[1]) * HC;                    // first unit of the problem
+  int n_tiles = tiles_of<kT>(a, b, room);
+  int hc = (int)((u0 - start) / n_tiles);
+  start += (int64_t)hc * n_tiles;
+
+  const float c2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // as in the prompt kernel
+  const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+  const gptr_t gk = (gptr_t)a.k, gv = (gptr_t)a.v;
+
+  for (int64_t u = u0; u < u1;) {
+    const int ta = (int)(u - start), tb = (int)min((int64_t)n_tiles, u1 - start);
+    const int hk = hc / chunks, h0 = hk * G + (hc % chunks) * kQ, nh = min(kQ, (hk + 1) * G - h0);
+    const int n_keys = (int)min((int64_t)max(a.lens[b], 0), room);
+    // (an empty sequence's row is never looked at; any readable word will do)
+    const int32_t* table = n_keys > 0 ? a.table + (int64_t)b * a.table_stride : a.lens;
+    const int64_t head_off = hk * a.head_stride;
+
+    bf16x8_t q[kNQ][kD / 32];
+#pragma unroll
+    for (int i = 0; i < kNQ; ++i)
+#pragma unroll
+      for (int s = 0; s < kD / 32; ++s) {
+        u32x4_t v = {0, 0, 0, 0};
+        if (16 * i + col < nh)
+          v = *(const u32x4_t*)(a.q + b * a.q_stride + (int64_t)(h0 + 16 * i + col) * kD + 32 * s + 8 * g);
+        q[i][s] = __builtin_bit_cast(bf16x8_t, v ^ u32x4_t{sign, sign, sign, sign});
+      }
+    f32x4_t o[kNQ][kNB];
+    float m[kNQ], mc[kNQ], lim[kNQ], l[kNQ];
+#pragma unroll
+    for (int i = 0; i < kNQ; ++i) {
+      m[i] = lim[i] = -INFINITY;
+      mc[i] = l[i] = 0.f;
+#pragma unroll
+      for (int n = 0; n < kNB; ++n) o[i][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // this wave's tiles are ta + w, ta + w + 4, ...: nt of them
+    const int nt = (tb - ta - w + kWaves - 1) / kWaves;
+    auto key_of = [&](int group) {   // this lane's key of the group; past the last tile, that tile's again
+      return (ta + w + kWaves * min(group * kGroup + lane / kT, nt - 1)) * kT + lane % kT;
+    };
+    auto page_of = [&](int group) {
+      const int key = key_of(group);
+      return table[key < n_keys ? key / a.page_size : 0];
+    };
+    // Lay out the rows of a group for its loads; returns which of its keys are seen, a bit for each lane.
+    auto rows = [&](int group, int page) {
+      const int key = key_of(group);
+      const bool valid = key < n_keys && page >= 0 && page < a.n_pages;
+      // a row that is not seen reads the cache's first row instead; what that holds is masked
+      const int64_t p = valid ? page : 0, slot = valid ? key % a.page_size : 0;
+      sRow[w][lane] = 2 * (head_off + p * a.page_stride + slot * a.slot_stride);
+      __builtin_amdgcn_wave_barrier();
+      return (uint64_t)__ballot(valid);
+    };
+    auto load = [&](int i, Stage& st) {   // tile i of the group in sRow
+      const int64_t* row = &sRow[w][i * kT + lane / kRowChunks];
+#pragma unroll
+      for (int x = 0; x < kDma; ++x) {
+        const int r = x * kDmaRows + lane / kRowChunks, c = lane % kRowChunks;
+        const int64_t off = row[x * kDmaRows];
+        __builtin_amdgcn_global_load_lds((gvoid_t)(gk + off + ((c ^ k_swz<kD>(r)) << 4)), (lds_ptr_t)(st.k + x * 1024), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((gvoid_t)(gv + off + ((c ^ v_swz<kD>(r)) << 4)), (lds_ptr_t)(st.v + x * 1024), 16, 0, 0);
+      }
+      __builtin_amdgcn_wave_barrier();
+    };
+    auto compute = [&](uint32_t seen, Stage& st) {
+      f32x4_t s[kNQ][kS];
+#pragma unroll
+      for (int h = 0; h < kS; ++h)
+#pragma unroll
+        for (int x = 0; x < kD / 32; ++x) {
+          const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(st.k + (16 * h + col) * kD * 2 + (((4 * x + g) ^ k_swz<kD>(16 * h + col)) << 4));
+#pragma unroll
+          for (int i = 0; i < kNQ; ++i)
+            s[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i][x], x == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s[i][h], 0, 0, 0);
+        }
+      if (seen != (uint32_t)((1ull << kT) - 1)) {
+#pragma unroll
+        for (int i = 0; i < kNQ; ++i)
+#pragma unroll
+          for (int h = 0; h < kS; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!((seen >> (16 * h + 4 * g + j)) & 1)) s[i][h][j] = -INFINITY;
+        // values that are not seen become zeros (weight 0 would not silence a NaN)
+#pragma unroll
+        for (int x = 0; x < kDma; ++x)
+          if (!((seen >> (x * kDmaRows + lane / kRowChunks)) & 1))
+            *reinterpret_cast<u32x4_t*>(st.v + x * 1024 + lane * 16) = u32x4_t{0, 0, 0, 0};
+        __builtin_amdgcn_wave_barrier();
+      }
+      s16x4_t p[kNQ][kS];
+#pragma unroll
+      for (int i = 0; i < kNQ; ++i) {
+        float t = s[i][0][0];
+#pragma unroll
+        for (int h = 0; h < kS; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t = fmaxf(t, s[i][h][j]);
+        t = fmaxf(t, __shfl_xor(t, 16));
+        t = fmaxf(t, __shfl_xor(t, 32));
+        if (__any(t > lim[i])) {
+          const float mn = fmaxf(m[i], t), mcn = mn == -INFINITY ? 0.f : mn * c2;
+          const float f = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mc[i] - mcn);
+          m[i] = mn;
+          mc[i] = mcn;
+          lim[i] = mn == -INFINITY ? -INFINITY : mn + kSlack / c2;
+          l[i] *= f;
+#pragma unroll
+          for (int n = 0; n < kNB; ++n) o[i][n] *= f;
+        }
+#pragma unroll
+        for (int h = 0; h < kS; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][h][j], c2, -mc[i]));
+            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][h][j + 1], c2, -mc[i]));
+            l[i] += e0 + e1;
+            const auto two = __builtin_bit_cast(s16x2_t, __builtin_convertvector(f32x2_t{e0, e1}, bf16x2_t));
+            p[i][h][j] = two[0];
+            p[i][h][j + 1] = two[1];
+          }
+      }
+      const int key = 4 * g + (col >> 2), at0 = key * kD * 2 + ((((lane & 3) >> 1) ^ v_swz<kD>(key)) << 4) + (lane & 1) * 8;
+#pragma unroll
+      for (int h = 0; h < kS; ++h)
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) {   // chunks 2 n and 2 n + 1
+          const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(st.v + 16 * h * kD * 2 + (at0 ^ (n << 5))));
+#pragma unroll
+          for (int i = 0; i < kNQ; ++i) o[i][n] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, p[i][h], o[i][n], 0, 0, 0);
+        }
+      // every read of the stage has returned before the next DMA into it
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+
+    if (nt > 0) {
+      int page[kPages];
+      uint64_t cur[kPages], next[kPages];
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) page[i] = page_of(i);
+      auto issue = [&](int j, int i, uint64_t& seen, Stage& st) {   // tile j + i; i is a constant
+        if (i % kGroup == 0) {
+          const int group = (j + i) / kGroup;
+          seen = rows(group, page[i / kGroup % kPages]);
+          page[i / kGroup % kPages] = page_of(group + kPages);
+        }
+        load(i % kGroup, st);
+      };
+      issue(0, 0, cur[0], sA[w]);
+      issue(0, 1, cur[1 / kGroup % kPages], sB[w]);
+      issue(0, 2, cur[2 / kGroup % kPages], sC[w]);
+      auto step = [&](int j, int i, Stage& st, Stage& free) {       // tile j + i; i is a constant
+        wait_vm<2 * 2 * kDma>();
+        issue(j, i + 3, next[(i + 3) / kGroup % kPages], free);
+        compute((uint32_t)(cur[i / kGroup] >> (i % kGroup * kT)) & (uint32_t)((1ull << kT) - 1), st);
+      };
+      for (int j = 0;; j += kRing) {
+        step(j, 0, sA[w], sD[w]);
+        if (j + 1 == nt) break;
+        step(j, 1, sB[w], sA[w]);
+        if (j + 2 == nt) break;
+        step(j, 2, sC[w], sB[w]);
+        if (j + 3 == nt) break;
+        step(j, 3, sD[w], sC[w]);
+        if (j + 4 == nt) break;
+#pragma unroll
+        for (int i = 0; i < kPages; ++i) cur[i] = next[i];
+      }
+      wait_dma();   // the repeated loads too, before the stages are used for the join
+    }
+
+    // join the waves: each scales its output to the common maximum and leaves it in its stage
+    const int jl = fresh_lane(), jt = w * 64 + jl, jg = jl >> 4, jc = jl & 15;
+    const bool whole = ta == 0 && tb == n_tiles;
+    const int64_t w_first = start / chunk;
+    const int64_t slot = blockIdx.x * 2 + (blockIdx.x == w_first && start % chunk ? 1 : 0);
+    float* part = parts + slot * kSlotFloats;
+    const __amdgpu_buffer_rsrc_t rp = make_rsrc(part, kSlotFloats * 4);
+#pragma unroll
+    for (int i = 0; i < kNQ; ++i) {
+      l[i] += __shfl_xor(l[i], 16);
+      l[i] += __shfl_xor(l[i], 32);
+      if (jg == 0) {
+        sM[w][16 * i + jc] = m[i] == -INFINITY ? -INFINITY : mc[i];
+        sL[w][16 * i + jc] = l[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kNQ; ++i) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) M = fmaxf(M, sM[x][16 * i + jc]);
+      const float f = m[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mc[i] - M);
+      f32x4_t* mine = reinterpret_cast<f32x4_t*>(&sA[w]) + jc * (kD / 4);
+#pragma unroll
+      for (int n = 0; n < kNB; ++n) mine[(4 * n + jg) ^ jc] = o[i][n] * f;
+      __syncthreads();
+      for (int e = jt; e < 16 * kD / 4; e += kThreads) {
+        const int row = e / (kD / 4), at = e % (kD / 4), r = 16 * i + row;
+        if (r >= nh) continue;
+        float Mr = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int x = 0; x < kWaves; ++x) Mr = fmaxf(Mr, sM[x][r]);
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < kWaves; ++x) {
+          v += reinterpret_cast<const f32x4_t*>(&sA[x])[row * (kD / 4) + (at ^ row)];
+          const float mx = sM[x][r], lx = sL[x][r];
+          L += mx == -INFINITY ? lx : lx * __builtin_amdgcn_exp2f(mx - Mr);
+        }
+        if (whole) {
+          const float inv = 1.f / L;
+          v = L == 0.f ? f32x4_t{0.f, 0.f, 0.f, 0.f} : v * inv;
+          const int64_t to = ((int64_t)b * a.Hq + h0 + r) * kD + 4 * at;
+          if (a.out_f32)
+            *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + to) = v;
+          else
+            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{
+                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[0], v[1]}, bf16x2_t)),
+                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[2], v[3]}, bf16x2_t))};
+          if (a.lse && at == 0)
+            a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (Mr + __builtin_amdgcn_logf(L)) * kLn2;
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rp, (uint32_t)(r * kD + 4 * at) * 4, 0, kCpolSc1);
+          if (at == 0) {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(Mr), rp, (uint32_t)(kMaxRows * 128 + r) * 4, 0, kCpolSc1);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(L), rp, (uint32_t)(kMaxRows * 129 + r) * 4, 0, kCpolSc1);
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    if (!whole) {
+      // the parts went to the device's coherence point; once every wave's stores are acknowledged this workgroup counts
+      // itself in, and the last one of the problem joins all parts in order
+      const int64_t w_last = (start + n_tiles - 1) / chunk;
+      const int n_parts = (int)(w_last - w_first) + 1;
+      uint32_t* counter = counters + (int64_t)b * HC + hc;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (jt == 0) {
+        const uint32_t seen = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        last = seen == (uint32_t)n_parts - 1;
+        if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // ready for the next call
+      }
+      __syncthreads();
+      if (last) {
+        acquire_agent();
+        const int64_t s_first = w_first * 2 + (start % chunk ? 1 : 0);   // later parts lie in their workgroup's first slot
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(parts, (uint64_t)kGrid * 2 * kSlotFloats * 4);
+        for (int e = jt; e < nh * kD / 4; e += kThreads) {
+          const int r = e / (kD / 4), at = e % (kD / 4);
+          auto off = [&](int i, int f) {
+            return (uint32_t)(((i == 0 ? s_first : (w_first + i) * 2) * kSlotFloats + f) * 4);
+          };
+          auto word = [&](int i, int f) {
+            return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, off(i, f), 0, kCpolSc1));
+          };
+          float M = -INFINITY;
+#pragma unroll 4
+          for (int i = 0; i < n_parts; ++i) M = fmaxf(M, word(i, kMaxRows * 128 + r));
+          float L = 0.f;
+          f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int i = 0; i < n_parts; ++i) {
+            const float mi = word(i, kMaxRows * 128 + r), li = word(i, kMaxRows * 129 + r);
+            const f32x4_t x = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, off(i, r * kD + 4 * at), 0, kCpolSc1));
+            const float f = mi == -INFINITY ? (li == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mi - M);
+            L += li * f;
+            v += x * f;
+          }
+          const float inv = 1.f / L;
+          v = L == 0.f ? f32x4_t{0.f, 0.f, 0.f, 0.f} : v * inv;
+          const int64_t to = ((int64_t)b * a.Hq + h0 + r) * kD + 4 * at;
+          if (a.out_f32)
+            *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + to) = v;
+          else
+            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{
+                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[0], v[1]}, bf16x2_t)),
+                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[2], v[3]}, bf16x2_t))};
+          if (a.lse && at == 0)
+            a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+        }
+      }
+    }
+
+    // next problem
+    u = start + tb;
+    if (u < u1) {
+      start += n_tiles;
+      if (++hc == HC) {
+        hc = 0;
+        n_tiles = tiles_of<kT>(a, ++b, room);
+      }
+    }
+  }
+}
+
+constexpr int64_t kPartBytes = (int64_t)kGrid * 2 * kSlotFloats * 4;
+
+int chunks_of(int Hq, int Hkv) { return (Hq / Hkv + kMaxRows - 1) / kMaxRows; }
+
+template <int kD, int kNQ>
+hipError_t launch(const DecodeArgs& a, hipStream_t stream) {
+  const int chunks = chunks_of(a.Hq, a.Hkv);
+  // no more workgroups than the longest possible lengths give ranges
+  const int64_t most = (int64_t)a.B * a.Hkv * chunks * (((int64_t)a.max_pages * a.page_size + tile_keys<kD>() - 1) / tile_keys<kD>() + 1);
+  const int64_t grid = min((int64_t)kGrid, (most + kMinTiles - 1) / kMinTiles);
+  float* parts = static_cast<float*>(a.workspace);
+  attn_decode_kernel<kD, kNQ><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(
+      a, chunks, parts, reinterpret_cast<uint32_t*>(static_cast<char*>(a.workspace) + kPartBytes));
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t attn_decode_workspace(int, int, int, int) { return 16; }
+// The parts' slots have one size whatever the call, so the counters behind them stay zero between calls of any shape.
+int64_t attn_decode_workspace(int B, int Hq, int Hkv, int) {
+  return kPartBytes + ((int64_t)B * Hkv * chunks_of(Hq, Hkv) * 4 + 15) / 16 * 16;
+}
 
 hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t stream) {
-  const unsigned grid = (unsigned)(((int64_t)a.B * a.Hq + kWaves - 1) / kWaves);
-  if (a.D == 64)
-    attn_decode_kernel<64><<<dim3(grid), dim3(64 * kWaves), 0, stream>>>(a);
-  else
-    attn_decode_kernel<128><<<dim3(grid), dim3(64 * kWaves), 0, stream>>>(a);
-  return hipGetLastError();
+  if (a.Hq / a.Hkv <= 16) return a.D == 64 ? launch<64, 1>(a, stream) : launch<128, 1>(a, stream);
+  return a.D == 64 ? launch<64, 2>(a, stream) : launch<128, 2>(a, stream);
 }
 
 }  // namespace sgt
