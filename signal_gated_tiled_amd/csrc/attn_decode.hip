@@ -7,7 +7,8 @@
 // Split and join.  The work is a list of problems (sequence, key head, chunk of
 // query heads), each a row of tiles of 2 KiB / D keys; the tiles of all problems,
 // one after another, are cut into equal ranges, one per workgroup, whatever the
-// lengths.  A workgroup that holds all of a problem's tiles writes the result; else
+// lengths (a problem counts kProblemCost tiles more than it has, for the latency of
+// its start and its join).  A workgroup that holds all of a problem's tiles writes the result; else
 // it writes its part (unnormalised output, maximum, sum) to the workspace and counts
 // itself in, and the last one to do so joins the parts in their order, so the
 // bits do not depend on who came last.
@@ -39,6 +40,7 @@ constexpr int kRing = 4;                      // LDS stages of a wave
 constexpr int kGrid = 256;                   // workgroups: one on each CU (128 KiB of LDS)
 constexpr int kMinTiles = 4;                 // tiles of a range at least: one for each wave
 constexpr int kMaxParts = 64;                // a problem is cut into about this many parts at most
+constexpr int kProblemCost = 16;             // what starting and joining a problem costs a workgroup, in tiles
 constexpr int kMaxRows = 32;                 // query heads of a chunk
 constexpr int kSlotFloats = kMaxRows * 128 + 2 * kMaxRows;   // one part: outputs, maxima, sums
 constexpr float kSlack = 8.f;                // log2 of the largest weight before the maximum moves
@@ -135,13 +137,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   const int G = a.Hq / a.Hkv, HC = a.Hkv * chunks;
   const int64_t room = (int64_t)a.max_pages * a.page_size;
 
-  // this workgroup's range of the units (tiles of all problems in order)
+  // this workgroup's range of the units (of each problem its tiles, then its cost)
   int64_t total = 0;
   int top = 0;
   for (int c = 0; c < a.B; c += kThreads) {
     const int n = tiles_of<kT>(a, c + tid, room);
     int64_t t;
-    block_scan(n, red, &t);
+    block_scan(n > 0 ? n + kProblemCost : 0, red, &t);
     total += t;
     top = max(top, n);
   }
@@ -161,27 +163,27 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   for (int64_t c = 0, before = 0; c < a.B; c += kThreads) {
     const int n = tiles_of<kT>(a, (int)c + tid, room);
     int64_t t;
-    const int64_t end = before + block_scan(n, red, &t);
-    if (n > 0 && (end - n) * HC <= u0 && u0 < end * HC) {
+    const int cost = n > 0 ? n + kProblemCost : 0;
+    const int64_t end = before + block_scan(cost, red, &t);
+    if (n > 0 && (end - cost) * HC <= u0 && u0 < end * HC) {
       found[0] = c + tid;
-      found[1] = end - n;
+      found[1] = end - cost;
     }
     before += t;
     if (before * HC > u0) break;
   }
   __syncthreads();
   int b = uniform((int)found[0]);
-  int64_t start = uniform(found[1]) * HC;                    // first unit of the problem
+  int64_t start = uniform(found[1]) * HC;   // first unit of the problem
   int n_tiles = tiles_of<kT>(a, b, room);
-  int hc = (int)((u0 - start) / n_tiles);
-  start += (int64_t)hc * n_tiles;
+  int hc = (int)((u0 - start) / (n_tiles + kProblemCost));
+  start += (int64_t)hc * (n_tiles + kProblemCost);
 
   const float c2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // as in the prompt kernel
   const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
   const gptr_t gk = (gptr_t)a.k, gv = (gptr_t)a.v;
 
-  for (int64_t u = u0; u < u1;) {
-    const int ta = (int)(u - start), tb = (int)min((int64_t)n_tiles, u1 - start);
+  auto problem = [&](int ta, int tb) {   // its tiles ta .. tb - 1
     const int hk = hc / chunks, h0 = hk * G + (hc % chunks) * kQ, nh = min(kQ, (hk + 1) * G - h0);
     const int n_keys = (int)min((int64_t)max(a.lens[b], 0), room);
     // (an empty sequence's row is never looked at; any readable word will do)
@@ -462,14 +464,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       }
     }
 
-    // next problem
-    u = start + tb;
-    if (u < u1) {
-      start += n_tiles;
-      if (++hc == HC) {
-        hc = 0;
-        n_tiles = tiles_of<kT>(a, ++b, room);
-      }
+  };
+
+  while (true) {
+    // the problem's tiles in this range; none if only the tail that stands for its cost lies here
+    const int ta = (int)max(u0 - start, (int64_t)0), tb = (int)min((int64_t)n_tiles, u1 - start);
+    if (ta < tb) problem(ta, tb);
+    start += n_tiles + kProblemCost;
+    if (start >= u1) break;
+    if (++hc == HC) {
+      hc = 0;
+      n_tiles = tiles_of<kT>(a, ++b, room);
     }
   }
 }
@@ -482,7 +487,7 @@ template <int kD, int kNQ>
 hipError_t launch(const DecodeArgs& a, hipStream_t stream) {
   const int chunks = chunks_of(a.Hq, a.Hkv);
   // no more workgroups than the longest possible lengths give ranges
-  const int64_t most = (int64_t)a.B * a.Hkv * chunks * (((int64_t)a.max_pages * a.page_size + tile_keys<kD>() - 1) / tile_keys<kD>() + 1);
+  const int64_t most = (int64_t)a.B * a.Hkv * chunks * (((int64_t)a.max_pages * a.page_size + tile_keys<kD>() - 1) / tile_keys<kD>() + 1 + kProblemCost);
   const int64_t grid = min((int64_t)kGrid, (most + kMinTiles - 1) / kMinTiles);
   float* parts = static_cast<float*>(a.workspace);
   attn_decode_kernel<kD, kNQ><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(
