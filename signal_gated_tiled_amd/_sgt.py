@@ -312,26 +312,37 @@ def gemm_rs_static_scratch_bytes() -> int:
     return int(lib().sgt_gemm_rs_static_scratch_bytes())
 
 
-def _layer_ptr(t, name: str, dtype, shape=None, device=None) -> int:
-    """Device pointer of a dense tensor of this dtype (and shape) on `device`; None is NULL."""
+def _layer_ptr(t, name: str, dtype, shape, device: int) -> int:
+    """Device pointer of a dense tensor of this dtype and shape on GPU `device`; None is NULL."""
     if t is None:
         return 0
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    return _dev_ptr(t, name, device)
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, expected GPU %d" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
-def _current_device(t, name: str):
-    """The device of `t`, which must be the calling thread's current GPU (the layer operators run there)."""
+def _current_device(t, name: str) -> int:
+    """The GPU of `t`, which must be the calling thread's current one (the layer operators run there)."""
     import torch
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("%s must be a GPU tensor" % name)
-    if torch.cuda.current_device() != t.device.index:
+    if torch.cuda.current_device() != dev:
         raise ValueError("the call runs on the current device (%d); %s is on %s" %
                          (torch.cuda.current_device(), name, t.device))
-    return t.device
+    return dev
+
+
+def _layer_stream(stream, device: int) -> int:
+    """Raw handle of `stream`, or of the device's current stream (without building a stream object for it)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: float = 1e-6, stream=None):
@@ -360,7 +371,7 @@ def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: f
                               _layer_ptr(weight, "weight", weight.dtype, (H,), dev), _dtype_code(weight),
                               _layer_ptr(out, "out", out.dtype, (T, H), dev), out_code,
                               _layer_ptr(scales, "scales", torch.float32, s_shape, dev), block, T, H, eps,
-                              _stream_handle(stream)))
+                              _layer_stream(stream, dev)))
 
 
 def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_group: int = 1, topk_group: int = 1,
@@ -381,7 +392,7 @@ def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_gro
                               _layer_ptr(bias, "bias", torch.float32, (E,), dev),
                               _layer_ptr(topk_ids, "topk_ids", torch.int32, (T, k), dev),
                               _layer_ptr(gate, "gate", torch.float32, (T, k), dev), T, E, k, SCORES[score], n_group,
-                              topk_group, group_top, 1 if renormalize else 0, scale, _stream_handle(stream)))
+                              topk_group, group_top, 1 if renormalize else 0, scale, _layer_stream(stream, dev)))
 
 
 def _heads(t, name: str, dev):
@@ -389,8 +400,8 @@ def _heads(t, name: str, dev):
     import torch
     if t.dtype != torch.bfloat16:
         raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, expected GPU %d" % (name, t.device, dev))
     st = t.stride()
     if len(st) != 3 or st[2] != 1:
         raise ValueError("%s must be tokens x heads x D with contiguous heads" % name)
@@ -406,14 +417,14 @@ def attn_prompt(q, k, v, out, cu_q, cu_k, *, lse=None, causal: bool = True, scal
     qp, kp, vp = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
     total_q, Hq, D = q.shape
     total_k, Hkv = k.shape[0], k.shape[1]
-    if tuple(k.shape) != tuple(v.shape) or k.shape[2] != D:
+    if k.shape != v.shape or k.shape[2] != D:
         raise ValueError("k %s and v %s do not match q %s" % (tuple(k.shape), tuple(v.shape), tuple(q.shape)))
     n = cu_q.shape[0] - 1
     _check(lib().sgt_attn_prompt(*qp, *kp, *vp, _layer_ptr(out, "out", torch.bfloat16, (total_q, Hq, D), dev),
                                  _layer_ptr(lse, "lse", torch.float32, (total_q, Hq), dev),
                                  _layer_ptr(cu_q, "cu_q", torch.int32, (n + 1,), dev),
                                  _layer_ptr(cu_k, "cu_k", torch.int32, (n + 1,), dev), n, total_q, total_k, Hq, Hkv, D,
-                                 1 if causal else 0, D ** -0.5 if scale is None else scale, _stream_handle(stream)))
+                                 1 if causal else 0, D ** -0.5 if scale is None else scale, _layer_stream(stream, dev)))
 
 
 def attn_decode_workspace(B: int, Hq: int, Hkv: int, D: int) -> int:
@@ -438,23 +449,23 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, workspace, *, l
         raise ValueError("the heads of q must lie side by side")
     if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
         raise TypeError("the caches must be bfloat16, got %s and %s" % (k_cache.dtype, v_cache.dtype))
-    if k_cache.device != dev or v_cache.device != dev:
-        raise ValueError("the caches are on %s and %s, expected %s" % (k_cache.device, v_cache.device, dev))
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("the caches are on %s and %s, expected GPU %d" % (k_cache.device, v_cache.device, dev))
     st = k_cache.stride()
     if len(st) != 4 or st[3] != 1 or v_cache.stride() != st or v_cache.shape != k_cache.shape or k_cache.shape[3] != D:
         raise ValueError("k_cache and v_cache must be n_pages x page_size x Hkv x D with the same strides")
     n_pages, page_size, Hkv = k_cache.shape[:3]
     if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or \
-            block_table.device != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be %d x max_pages int32 on %s with contiguous rows" % (B, dev))
+            block_table.get_device() != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be %d x max_pages int32 on GPU %d with contiguous rows" % (B, dev))
     max_pages = block_table.shape[1]
     _check(lib().sgt_attn_decode(q_ptr, q_stride, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n_pages,
                                  page_size, block_table.data_ptr(), block_table.stride(0) if B > 1 else max_pages,
                                  max_pages, _layer_ptr(seq_lens, "seq_lens", torch.int32, (B,), dev),
                                  _layer_ptr(out, "out", out.dtype, (B, Hq, D), dev), _dtype_code(out),
                                  _layer_ptr(lse, "lse", torch.float32, (B, Hq), dev),
-                                 _dev_ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
-                                 B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _stream_handle(stream)))
+                                 _layer_ptr(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.numel() * workspace.element_size(),
+                                 B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _layer_stream(stream, dev)))
 
 
 class Context:

@@ -29,6 +29,7 @@ struct GateArgs {
   int32_t E, k;
   int32_t n_group, topk_group, group_top;
   int32_t sigmoid, renormalize, bf16;
+  int32_t wide;         // rows can be read four logits at a time
   float scale;
 };
 

@@ -1,5 +1,15 @@
 // Routing of tokens to experts: softmax or sigmoid scores, a bias that takes
 // part in the choice only, groups of experts, top-k and renormalised weights.
+//
+// The logits are read once and little is written, so the choice itself bounds
+// this: kL lanes hold one token's experts, lane j the kSlots from j kSlots on, and
+// each of the k rounds finds the largest remaining choice value.  A value and its
+// expert are one positive double, made of the value's order-preserving 32-bit key and
+// the expert's number from the end, so that one v_max_f64 per value keeps the
+// larger one and, of equal ones, the lower expert; four of them over DPP exchanges
+// (16 lanes) finish a round for the four tokens of a wave at once.  The chosen
+// experts' scores are computed again from their logits at the end, which costs one
+// small gather instead of carrying every score through the rounds.
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
@@ -10,125 +20,244 @@ namespace sgt {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kMaxSlots = 16;   // 1024 experts over 64 lanes
 
-// (value, index) of the largest value over the wave, of equal ones the lowest index.
-__device__ __forceinline__ void wave_best(float& v, int& i) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float ov = __shfl_xor(v, o);
-    const int oi = __shfl_xor(i, o);
-    if (ov > v || (ov == v && oi < i)) {
-      v = ov;
-      i = oi;
-    }
-  }
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+// Order-preserving map of an fp32 value (not NaN) to uint32; -0 and +0 alike, as comparison has them.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  uint32_t u = __float_as_uint(f);
+  if (u == 0x80000000u) u = 0u;
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-constexpr int kNone = 0x7FFFFFFF;
+// The value's key in bits 61 .. 30 and kLast - e below: a positive double, never NaN, larger for a larger value and, of
+// equal ones, for a lower e.  (Double subnormals are kept.)  0 stands for nothing: every candidate is larger.
+constexpr uint32_t kLast = 2047;
+__device__ __forceinline__ double pack(float v, int e) {
+  return __builtin_bit_cast(double, ((uint64_t)order_key(v) << 30) | (kLast - (uint32_t)e));
+}
+__device__ __forceinline__ int expert_of(double p) {
+  return (int)(kLast - ((uint32_t)__builtin_bit_cast(uint64_t, p) & 0x3FFFFFFFu));
+}
 
-// One wave per token; lane l holds experts l, l + 64, ...
+template <int kCtrl> __device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <int kCtrl> __device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xF, 0xF, true));
+}
+
+// The bare instruction: fmax would first quieten NaNs that cannot be here, at three times the cost.
+__device__ __forceinline__ double larger(double a, double b) {
+  double m;
+  asm("v_max_f64 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
+  return m;
+}
+
+// Reduction over a token's kL lanes, the same in each: quad swaps, half-row and row mirrors, then the four rows.
+template <int kL, class T, class F> __device__ __forceinline__ T over_token(T v, F f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  if constexpr (kL == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + expf(-x)); }
+
+// exp(x - top): 1 for the largest logits themselves (+infinity too), 0 for -infinity.
+__device__ __forceinline__ float weight(float x, float top) { return x == top ? (top == -INFINITY ? 0.f : 1.f) : expf(x - top); }
+
+// NaN counts as -infinity.
+__device__ __forceinline__ float no_nan(float x) { return x == x ? x : -INFINITY; }
+
+__device__ __forceinline__ float logit(const GateArgs& a, int64_t t, int e) {
+  return no_nan(load_elem(a.logits, a.bf16 ? SGT_BF16 : SGT_F32, t * a.stride + e));
+}
+
+// kL lanes per token, kSlots experts per lane, kPicks choices per lane at most.
+template <int kL, int kSlots, int kPicks>
 __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
-  __shared__ float sc[kWaves][64 * kMaxSlots];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kWaves + wv;
-  if (t >= a.T) return;
-  float x[kMaxSlots], c[kMaxSlots], s[kMaxSlots];
-  bool live[kMaxSlots];
-  float top = -INFINITY;
+  constexpr int kTokens = 64 / kL;   // per wave
+  __shared__ float sc[kWaves * kTokens][kL * kSlots + 1];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, j = lane % kL, slot = wv * kTokens + lane / kL;
+  const int64_t t = (int64_t)blockIdx.x * (kWaves * kTokens) + slot;
+  const bool live = t < a.T;
+  const int64_t tc = live ? t : a.T - 1;   // lanes past the end repeat the last token and write nothing
+
+  float x[kSlots];
 #pragma unroll
-  for (int q = 0; q < kMaxSlots; ++q) {
-    const int e = lane + 64 * q;
-    live[q] = e < a.E;
-    x[q] = live[q] ? load_elem(a.logits, a.bf16 ? SGT_BF16 : SGT_F32, t * a.stride + e) : -INFINITY;
-    if (x[q] != x[q]) x[q] = -INFINITY;
-    top = fmaxf(top, x[q]);
-  }
-  top = wave_max(top);
-  float total = 0.f;
+  for (int q = 0; q < kSlots; ++q) x[q] = -INFINITY;
+  if (a.wide && (j + 1) * kSlots <= a.E) {
+    const int64_t at = tc * a.stride + j * kSlots;
 #pragma unroll
-  for (int q = 0; q < kMaxSlots; ++q) {
-    if (a.sigmoid)
-      s[q] = 1.f / (1.f + expf(-x[q]));
-    else
-      s[q] = x[q] == top ? (top == -INFINITY ? 0.f : 1.f) : expf(x[q] - top);
-    if (!live[q]) s[q] = 0.f;
-    total += s[q];
+    for (int q = 0; q < kSlots; q += 4) {
+      if (a.bf16) {
+        const u32x2_t v = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(a.logits) + at + q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[q + i] = no_nan(bf16_to_f32((uint16_t)(v[i / 2] >> (16 * (i & 1)))));
+      } else {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.logits) + at + q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[q + i] = no_nan(v[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q)
+      if (j * kSlots + q < a.E) x[q] = logit(a, tc, j * kSlots + q);
   }
+  float top = -INFINITY, inv = 0.f;
+  const bool scores = a.bias || (a.n_group > 1 && a.group_top > 1);
   if (!a.sigmoid) {
-    total = wave_sum(total);
-    const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
-    for (int q = 0; q < kMaxSlots; ++q) s[q] *= inv;
-  }
-  const bool by_score = a.bias != nullptr || (a.n_group > 1 && a.group_top > 1);
+    for (int q = 0; q < kSlots; ++q) top = fmaxf(top, x[q]);
+    top = over_token<kL>(top, [](float u, float v) { return fmaxf(u, v); });
+    float total = 0.f;
 #pragma unroll
-  for (int q = 0; q < kMaxSlots; ++q) {
-    const int e = lane + 64 * q;
-    c[q] = live[q] && a.bias ? s[q] + a.bias[e] : x[q];
-    if (c[q] != c[q]) c[q] = -INFINITY;
-    if (a.n_group > 1 && live[q]) sc[wv][e] = by_score ? (a.bias ? c[q] : s[q]) : x[q];
+    for (int q = 0; q < kSlots; ++q) total += weight(x[q], top);
+    total = over_token<kL>(total, [](float u, float v) { return u + v; });
+    inv = total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f;
   }
-  if (a.n_group > 1) {
-    const int per = a.E / a.n_group;
-    float g = -INFINITY;
-    if (lane < a.n_group) {
-      float b1 = -INFINITY, b2 = -INFINITY;
-      for (int j = 0; j < per; ++j) {
-        const float v = sc[wv][lane * per + j];
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
-      }
-      g = a.group_top > 1 ? b1 + b2 : b1;
+  auto score = [&](float v) { return a.sigmoid ? sigmoid(v) : weight(v, top) * inv; };
+
+  // Groups whose lanes are whole (kSlots divides a group, the group's lanes are 1, 2, 4, 8 or 16) are weighed in registers,
+  // others through LDS.
+  const int per = a.E / a.n_group, span = per / kSlots;
+  const bool grouped = a.n_group > 1, whole = kL == 16 && per % kSlots == 0 && (span & (span - 1)) == 0;
+  double c[kSlots];   // what is left to choose from
+  float b1 = -INFINITY, b2 = -INFINITY;
+  auto add = [&](float v) {   // the two largest so far
+    b2 = fmaxf(b2, fminf(b1, v));
+    b1 = fmaxf(b1, v);
+  };
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int e = j * kSlots + q;
+    float v = x[q], by = v;   // the choice value, and what its group is weighed by
+    if (scores) {
+      by = score(v);
+      if (a.bias) v = by = e < a.E ? no_nan(by + a.bias[e]) : -INFINITY;
     }
-    bool left = lane < a.n_group;
+    if (grouped) {
+      if (whole) add(by);
+      else sc[slot][e] = by;
+    }
+    c[q] = e < a.E ? pack(v, e) : 0.;
+  }
+
+  if (grouped) {
+    constexpr int kR = 64 / kL;
+    double g[kR];       // candidates: this lane's groups (several lanes may hold the same one)
+    int id[kR];
+    auto worth = [&] { return no_nan(a.group_top > 1 ? b1 + b2 : b1); };
+    if (whole) {
+      auto merge = [&](float o1, float o2) {
+        b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+        b1 = fmaxf(b1, o1);
+      };
+      if (span > 1) merge(dpp<0xB1>(b1), dpp<0xB1>(b2));
+      if (span > 2) merge(dpp<0x4E>(b1), dpp<0x4E>(b2));
+      if (span > 4) merge(dpp<0x141>(b1), dpp<0x141>(b2));
+      if (span > 8) merge(dpp<0x140>(b1), dpp<0x140>(b2));
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        g[r] = 0.;
+        id[r] = j / span;
+      }
+      if (id[0] < a.n_group) g[0] = pack(worth(), id[0]);
+    } else {
+      __builtin_amdgcn_wave_barrier();   // a token's lanes are one wave's
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        id[r] = j + kL * r;
+        g[r] = 0.;
+        if (id[r] < a.n_group) {
+          b1 = b2 = -INFINITY;
+          for (int i = 0; i < per; ++i) add(sc[slot][id[r] * per + i]);
+          g[r] = pack(worth(), id[r]);
+        }
+      }
+    }
     uint64_t kept = 0;
-    for (int j = 0; j < a.topk_group; ++j) {
-      float v = left ? g : -INFINITY;
-      int i = left ? lane : kNone;
-      wave_best(v, i);
-      kept |= 1ull << i;
-      if (lane == i) left = false;
-    }
+    for (int i = 0; i < a.topk_group; ++i) {
+      double m = g[0];
 #pragma unroll
-    for (int q = 0; q < kMaxSlots; ++q) {
-      const int e = lane + 64 * q;
-      if (live[q] && !((kept >> (e / per)) & 1)) live[q] = false;
+      for (int r = 1; r < kR; ++r) m = larger(m, g[r]);
+      m = over_token<kL>(m, larger);
+      const int best = expert_of(m);
+      kept |= 1ull << (best & 63);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) g[r] = id[r] == best ? 0. : g[r];
+    }
+    int group = j * kSlots / per, in = j * kSlots % per;
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      if (!((kept >> (group & 63)) & 1)) c[q] = 0.;
+      if (++in == per) {
+        in = 0;
+        ++group;
+      }
     }
   }
-  float sum = 0.f, mine = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    float v = -INFINITY;
-    int i = kNone;
+
+  int pick[kPicks] = {};   // lane j keeps choices j, j + kL, ...
+  for (int i = 0; i < a.k; ++i) {
+    double m = c[0];
 #pragma unroll
-    for (int q = 0; q < kMaxSlots; ++q)
-      if (live[q] && (i == kNone || c[q] > v)) {
-        v = c[q];
-        i = lane + 64 * q;
-      }
-    wave_best(v, i);
-    float w = 0.f;
+    for (int q = 1; q < kSlots; ++q) m = larger(m, c[q]);
+    m = over_token<kL>(m, larger);
+    const int e = expert_of(m);
 #pragma unroll
-    for (int q = 0; q < kMaxSlots; ++q)
-      if (lane + 64 * q == i) {
-        w = s[q];
-        live[q] = false;
-      }
-    w = __shfl(w, i & 63);
-    sum += w;
-    if (lane == j) {
-      mine = w;
-      a.ids[t * a.k + j] = i;
-    }
+    for (int q = 0; q < kSlots; ++q) c[q] = j * kSlots + q == e ? 0. : c[q];
+#pragma unroll
+    for (int r = 0; r < kPicks; ++r) pick[r] = j + kL * r == i ? e : pick[r];
   }
-  if (lane < a.k) a.gate[t * a.k + lane] = (a.renormalize ? (sum > 0.f ? mine / sum : 0.f) : mine) * a.scale;
+
+  float w[kPicks], sum = 0.f;
+#pragma unroll
+  for (int r = 0; r < kPicks; ++r) {
+    w[r] = j + kL * r < a.k ? score(logit(a, tc, pick[r])) : 0.f;
+    sum += w[r];
+  }
+  sum = over_token<kL>(sum, [](float u, float v) { return u + v; });
+  const float f = a.renormalize ? (sum > 0.f ? a.scale / sum : 0.f) : a.scale;
+  if (!live) return;
+#pragma unroll
+  for (int r = 0; r < kPicks; ++r)
+    if (j + kL * r < a.k) {
+      a.ids[t * a.k + j + kL * r] = pick[r];
+      a.gate[t * a.k + j + kL * r] = w[r] * f;
+    }
+}
+
+template <int kL, int kSlots>
+hipError_t launch(const GateArgs& a, hipStream_t stream) {
+  constexpr int kTokens = kWaves * 64 / kL;
+  const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(64 * kWaves);
+  if (a.k <= kL)
+    moe_gate_kernel<kL, kSlots, 1><<<grid, block, 0, stream>>>(a);
+  else
+    moe_gate_kernel<kL, kSlots, (64 + kL - 1) / kL><<<grid, block, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_moe_gate(const GateArgs& a, hipStream_t stream) {
-  moe_gate_kernel<<<dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0, stream>>>(a);
-  return hipGetLastError();
+  // 16 lanes take a token of up to 256 experts, so that a round's exchanges serve four tokens; more experts a whole wave
+  if (a.E <= 64) return launch<16, 4>(a, stream);
+  if (a.E <= 128) return launch<16, 8>(a, stream);
+  if (a.E <= 256) return launch<16, 16>(a, stream);
+  return launch<64, 16>(a, stream);
 }
 
 }  // namespace sgt
