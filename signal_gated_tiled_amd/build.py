@@ -31,7 +31,7 @@ FLAGS = [
 
 # Flags of one file.  The decode kernel's LDS leaves one wave per SIMD, from which the compiler would conclude that the
 # matrix products had better accumulate in the second half of the register file, and copy its values to and fro.
-FILE_FLAGS = {"attn_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+FILE_FLAGS = {"attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"], "attn_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def sources():

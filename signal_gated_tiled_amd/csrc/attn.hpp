@@ -1,0 +1,48 @@
+// What the prompt and decode attention kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "elem.hpp"
+#include "mfma_tile.hpp"
+
+namespace sgt {
+
+// The running maximum of a row's scores moves only when a weight would pass 2^kSlack: weights up to that cost neither
+// the fp32 sums nor the bf16 products anything, and the accumulators are rarely rescaled.
+constexpr float kSlack = 8.f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+typedef short s16x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_ptr;
+
+// Exponent (of 2) of a weight per unit of score.  Scale 0 becomes a factor that rounds every finite score away, but
+// still takes -infinity to weight 0; a negative scale's sign goes to the queries.
+__device__ __forceinline__ float weight_exponent(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1e-30f); }
+__device__ __forceinline__ uint32_t query_sign(float scale) { return scale < 0.f ? 0x80008000u : 0u; }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+}
+
+// A value that all lanes share, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v);
+  return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | lo);
+}
+
+// Wait until at most n vector memory operations of this wave are outstanding.  The builtin, so that the compiler counts
+// with it: behind an asm wait it would wait again, for everything, before it reads LDS that a DMA has filled.
+template <int n> __device__ __forceinline__ void wait_vm() {
+  static_assert(n < 64, "vmcnt has 6 bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);   // expcnt and lgkmcnt at their maxima
+  asm volatile("" ::: "memory");
+}
+
+}  // namespace sgt

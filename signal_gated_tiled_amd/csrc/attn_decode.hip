@@ -26,9 +26,8 @@
 // pass 2^8.
 #include <hip/hip_runtime.h>
 
-#include "elem.hpp"
+#include "attn.hpp"
 #include "layer.hpp"
-#include "mfma_tile.hpp"
 #include "signal.hpp"
 
 namespace sgt {
@@ -43,15 +42,7 @@ constexpr int kMaxParts = 64;                // a problem is cut into about this
 constexpr int kProblemCost = 16;             // what starting and joining a problem costs a workgroup, in tiles
 constexpr int kMaxRows = 32;                 // query heads of a chunk
 constexpr int kSlotFloats = kMaxRows * 128 + 2 * kMaxRows;   // one part: outputs, maxima, sums
-constexpr float kSlack = 8.f;                // log2 of the largest weight before the maximum moves
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef short s16x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_ptr;
 typedef const __attribute__((address_space(1))) uint8_t* gptr_t;
 typedef const __attribute__((address_space(1))) void* gvoid_t;
 
@@ -69,13 +60,6 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int64_t room
   if (b >= a.B) return 0;
   const int64_t n = min((int64_t)max(a.lens[b], 0), room);
   return (int)max((n + kT - 1) / kT, (int64_t)1);   // an empty sequence is one tile of unseen keys
-}
-
-// A value that all lanes share, in scalar registers.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v);
-  return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | lo);
 }
 
 // Inclusive prefix sum over the workgroup and its total; `red` holds kWaves words.
@@ -97,15 +81,6 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* 
   }
   *total = all;
   return v;
-}
-
-// Wait until at most n vector memory operations are outstanding.
-// (the builtin, so that the compiler counts with it; the operand's other counters are left alone).
-template <int n> __device__ __forceinline__ void wait_vm() {
-  static_assert(n < 64, "vmcnt has 6 bits");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);
-  asm volatile("" ::: "memory");
 }
 
 // The lane's number, hidden from the optimiser: what is computed from it stays where it is used (rare paths, or one
@@ -179,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   int hc = (int)((u0 - start) / (n_tiles + kProblemCost));
   start += (int64_t)hc * (n_tiles + kProblemCost);
 
-  const float c2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);   // as in the prompt kernel
-  const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+  const float c2 = weight_exponent(a.scale);
+  const uint32_t sign = query_sign(a.scale);
   const gptr_t gk = (gptr_t)a.k, gv = (gptr_t)a.v;
 
   auto problem = [&](int ta, int tb) {   // its tiles ta .. tb - 1
@@ -344,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
 #pragma unroll
         for (int i = 0; i < kPages; ++i) cur[i] = next[i];
       }
-      wait_dma();   // the repeated loads too, before the stages are used for the join
+      wait_vm<0>();   // the repeated loads too, before the stages are used for the join
     }
 
     // join the waves: each scales its output to the common maximum and leaves it in its stage
@@ -394,9 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
           if (a.out_f32)
             *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + to) = v;
           else
-            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{
-                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[0], v[1]}, bf16x2_t)),
-                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[2], v[3]}, bf16x2_t))};
+            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
           if (a.lse && at == 0)
             a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (Mr + __builtin_amdgcn_logf(L)) * kLn2;
         } else {
@@ -455,9 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
           if (a.out_f32)
             *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + to) = v;
           else
-            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{
-                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[0], v[1]}, bf16x2_t)),
-                __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{v[2], v[3]}, bf16x2_t))};
+            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
           if (a.lse && at == 0)
             a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
         }

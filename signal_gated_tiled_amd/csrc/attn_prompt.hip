@@ -29,22 +29,13 @@
 // seen tiles zeroed, and recomputes by plain loops the rows that really see one.
 #include <hip/hip_runtime.h>
 
-#include "elem.hpp"
+#include "attn.hpp"
 #include "layer.hpp"
-#include "mfma_tile.hpp"
 
 namespace sgt {
 
 namespace {
 
-constexpr int kKeys = 64;                    // keys per tile
-constexpr float kSlack = 8.f;                // log2 of the largest weight before m moves
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_ptr;
 
 // Chunk swizzles of the K and V tiles (rows of kD * 2 bytes).
 template <int kD> __device__ __forceinline__ int k_swz(int row) { return kD == 128 ? (row & 15) : ((row >> 1) & 7); }
@@ -92,6 +83,7 @@ __device__ __forceinline__ Tile1 find_tile(const PromptArgs& a, int w, int G, in
   for (int c = 64; c < a.n_seqs; c += 64) top = max(top, seq_tiles(a, c + lane, G, rows));
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
+  top = uniform(top);
   auto above = [&](int level) {   // tiles at levels >= level
     int n = max(mine - level, 0);
     if (!one)
@@ -100,35 +92,38 @@ __device__ __forceinline__ Tile1 find_tile(const PromptArgs& a, int w, int G, in
   };
   Tile1 t{};
   t.seq = -1;
-  if (above(0) <= w) return t;
+  if (uniform(above(0)) <= w) return t;
   int lo = 0, hi = top;           // above(lo) > w, above(hi) = 0
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (above(mid) > w) lo = mid; else hi = mid;
+    if (uniform(above(mid)) > w) lo = mid; else hi = mid;
   }
-  int k = w - above(lo + 1);      // place inside level lo
+  int k = w - uniform(above(lo + 1));      // place inside level lo
+  int s = 0;
   for (int c = 0; c < a.n_seqs; c += 64) {
     uint64_t has = __ballot((c == 0 ? mine : seq_tiles(a, c + lane, G, rows)) > lo);
     const int n = __popcll(has);
-    if (k >= n) {
-      k -= n;
-      continue;
+    if (k < n) {
+      for (; k > 0; --k) has &= has - 1;
+      s = c + __ffsll((unsigned long long)has) - 1;
+      break;
     }
-    for (; k > 0; --k) has &= has - 1;
-    const int s = c + __ffsll((unsigned long long)has) - 1;
-    t.seq = s;
-    t.tile = lo;
-    t.q0 = min(max((int64_t)a.cu_q[s], (int64_t)0), a.total_q);
-    t.Lq = (int)(min(max((int64_t)a.cu_q[s + 1], t.q0), a.total_q) - t.q0);
-    t.k0 = min(max((int64_t)a.cu_k[s], (int64_t)0), a.total_k);
-    t.Lk = (int)(min(max((int64_t)a.cu_k[s + 1], t.k0), a.total_k) - t.k0);
-    break;
+    k -= n;
   }
+  // uniform in fact; said so, since buffer resources and loop bounds are built from them (per lane, each load would be
+  // a loop over the lanes' resources)
+  s = uniform(s);
+  t.seq = s;
+  t.tile = uniform(lo);
+  t.q0 = uniform(min(max((int64_t)a.cu_q[s], (int64_t)0), a.total_q));
+  t.Lq = uniform((int)(min(max((int64_t)a.cu_q[s + 1], t.q0), a.total_q) - t.q0));
+  t.k0 = uniform(min(max((int64_t)a.cu_k[s], (int64_t)0), a.total_k));
+  t.Lk = uniform((int)(min(max((int64_t)a.cu_k[s + 1], t.k0), a.total_k) - t.k0));
   return t;
 }
 
 // DMA of one operand's tiles: kW waves fill kKeys rows of kD bf16.
-template <int kD, int kW, bool kIsV>
+template <int kD, int kW, int kKeys, bool kIsV>
 struct TileDma {
   static constexpr int kLoads = kKeys * kD * 2 / 1024 / kW;   // 1 KiB loads per wave
   static constexpr int kRowChunks = kD / 8, kRowsPerLoad = 64 / kRowChunks;
@@ -149,15 +144,35 @@ struct TileDma {
       off[i] = (uint32_t)(row * stride + chunk * 16);
     }
   }
-  // Rows past the sequence's end lie past the records and read as zero.
-  __device__ __forceinline__ void issue(uint8_t* stage, int j0) const {
+  // The tile from key j0 on.  Rows past the sequence's end lie past the records and read as zero.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t at(int j0) const {
     const int rows = min(Lk - j0, kKeys);
     const char* p = reinterpret_cast<const char*>(base) + j0 * stride;
-    const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(p, rows > 0 ? (uint64_t)(rows - 1) * stride + kD * 2 : 0);
+    return make_rsrc(p, rows > 0 ? (uint64_t)(rows - 1) * stride + kD * 2 : 0);
+  }
+  __device__ __forceinline__ void one(__amdgpu_buffer_rsrc_t rsrc, uint8_t* stage, int i) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(stage + (wave_id() * kLoads + i) * 1024), 16, off[i], 0, 0, 0);
+  }
+  __device__ __forceinline__ void issue(uint8_t* stage, int j0) const {
+    const __amdgpu_buffer_rsrc_t rsrc = at(j0);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(stage + (wave_id() * kLoads + i) * 1024), 16, off[i],
-                                               0, 0, 0);
+    for (int i = 0; i < kLoads; ++i) one(rsrc, stage, i);
+  }
+};
+
+// The loads of a step: kLoads of a tile of keys, then of a tile of values, in kD / 32 parts.
+template <int kD, int kW, int kKeys>
+struct NextTiles {
+  const TileDma<kD, kW, kKeys, false>& kd;
+  const TileDma<kD, kW, kKeys, true>& vd;
+  __amdgpu_buffer_rsrc_t rk, rv;
+  uint8_t *sK, *sV;
+  __device__ __forceinline__ void part(int i) const {
+    constexpr int kLoads = TileDma<kD, kW, kKeys, false>::kLoads, kPer = 2 * kLoads * 32 / kD;
+#pragma unroll
+    for (int x = i * kPer; x < (i + 1) * kPer; ++x)
+      if (x < kLoads) kd.one(rk, sK, x);
+      else vd.one(rv, sV, x - kLoads);
   }
 };
 
@@ -169,39 +184,44 @@ struct RowState {
   float mc;              // m in the weights' exponent, or 0 while m is -infinity
 };
 
-// One key tile: scores, weights, products.  `seen` is how many of the tile's
-// keys this lane's row sees when kMask (from the first key on).
-template <int kD>
-__device__ __forceinline__ void tile_step(const uint8_t* sK, const uint8_t* sV, const bf16x8_t (&q)[kD / 16],
-                                          RowState<kD>& st, const uint32_t (&ka)[kD / 16], const uint32_t (&va)[kD / 32],
-                                          float c, bool mask, int seen) {
-  const int half = (threadIdx.x >> 5) & 1;
-  f32x16_t s[2];
-#pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
+// S^T of a key tile.
+template <int kD, int kB>
+__device__ __forceinline__ void scores(const uint8_t* sK, const bf16x8_t (&q)[kD / 16], uint32_t ka,
+                                       f32x16_t (&s)[kB]) {
 #pragma unroll
   for (int t = 0; t < kD / 16; ++t)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(sK + ka[t] + b * 32 * kD * 2);
-      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[t], s[b], 0, 0, 0);
+    for (int b = 0; b < kB; ++b) {
+      const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(sK + (ka ^ (t << 5)) + b * 32 * kD * 2);
+      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[t], t == 0 ? f32x16_t{} : s[b], 0, 0, 0);
     }
-  if (mask) {
+}
+
+// Only the first `seen` keys of the tile count for this lane's row.
+template <int kB> __device__ __forceinline__ void mask_scores(f32x16_t (&s)[kB], int seen) {
+  const int half = (threadIdx.x >> 5) & 1;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < kB; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int key = 32 * b + 8 * (r / 4) + 4 * half + r % 4;
-        s[b][r] = key < seen ? s[b][r] : -INFINITY;
-      }
-  }
-  float top = fmaxf(s[0][0], s[1][0]);
+    for (int r = 0; r < 16; ++r) {
+      const int key = 32 * b + 8 * (r / 4) + 4 * half + r % 4;
+      s[b][r] = key < seen ? s[b][r] : -INFINITY;
+    }
+}
+
+// The row's largest of the scores r0 .. r0 + n - 1 of each block, and `top` (of this lane's half of the keys).
+template <int kB> __device__ __forceinline__ float top_score(const f32x16_t (&s)[kB], int r0, int n, float top) {
 #pragma unroll
-  for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(s[0][r], s[1][r]), top);
-  top = fmaxf(top, other_half(top));
-  if (__any(top > st.limit)) {
+  for (int r = r0; r < r0 + n; r += 3 - kB)
+    top = fmaxf(fmaxf(s[0][r], kB == 2 ? s[kB - 1][r] : s[0][r + 1]), top);
+  return top;
+}
+
+// Move the maximum where a weight would pass 2^kSlack.
+template <int kD>
+__device__ __forceinline__ void move_max(RowState<kD>& st, float top, float c) {
+  if (__any(top > st.limit)) {   // in either half of the keys
+    top = fmaxf(top, other_half(top));
     const float m = fmaxf(st.m, top), mc = m == -INFINITY ? 0.f : m * c;
     const float f = st.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.mc - mc);
     st.m = m;
@@ -213,32 +233,88 @@ __device__ __forceinline__ void tile_step(const uint8_t* sK, const uint8_t* sV, 
 #pragma unroll
       for (int r = 0; r < 16; ++r) st.o[b][r] *= f;
   }
-  bf16x8_t p[4];   // product step t covers keys 16 t .. 16 t + 15
+}
+
+// Weights of elements [kAt, kAt + kN) of a tile's 16 kB per lane; product step t covers keys 16 t .. 16 t + 15.
+template <int kD, int kB, int kAt, int kN>
+__device__ __forceinline__ void weights(const f32x16_t (&s)[kB], RowState<kD>& st, float c, u32x4_t (&p)[2 * kB]) {
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int i = kAt; i < kAt + kN; i += 2) {
+    const int b = i / 16, r = i % 16;
+    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, -st.mc));
+    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r + 1], c, -st.mc));
+    st.l += e0 + e1;
+    uint32_t two = pack_bf16(e0, e1);
+    asm volatile("" : "+v"(two));   // computed here, beside the next scores, and not where it is first used
+    p[i / 8][i % 8 / 2] = two;
+  }
+  asm volatile("" : "+v"(st.l));   // summed here, or the weights would stay in registers until they are
+}
+
+// V^T of product step t, all column blocks.
+template <int kD>
+__device__ __forceinline__ void read_v(const uint8_t* sV, uint32_t va, int t, bf16x8_t (&v)[kD / 32]) {
 #pragma unroll
-    for (int r = 0; r < 16; r += 2) {
-      const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, -st.mc));
-      const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r + 1], c, -st.mc));
-      st.l += e0 + e1;
-      const bf16x2_t two = __builtin_convertvector(f32x2_t{e0, e1}, bf16x2_t);
-      p[2 * b + r / 8][r % 8] = two[0];
-      p[2 * b + r / 8][r % 8 + 1] = two[1];
+  for (int b = 0; b < kD / 32; ++b) {
+    const uint8_t* at = sV + (va ^ (b << 6)) + t * 16 * kD * 2;
+    const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(at));
+    const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(at + 8 * kD * 2));
+    v[b] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+}
+
+template <int kD, int kB>
+__device__ __forceinline__ void read_k(const uint8_t* sK, uint32_t ka, int t, bf16x8_t (&k)[kB]) {
+#pragma unroll
+  for (int b = 0; b < kB; ++b) k[b] = *reinterpret_cast<const bf16x8_t*>(sK + (ka ^ (t << 5)) + b * 32 * kD * 2);
+}
+
+// The scores of the next tile beside the weights of the current one, in groups of kB matrix instructions and their
+// share of the weights; the reads of a group's operands go one group ahead.  The scheduling barriers keep the order.
+// A part of the next tiles' DMA goes behind every second group: in a burst the loads would back up the wave's issue
+// behind the CU's load path.
+template <int kD, int kB, int kT = 0, class Loads>
+__device__ __forceinline__ void scores_and_weights(const uint8_t* sK, const uint8_t* sV, const bf16x8_t (&q)[kD / 16],
+                                                   uint32_t ka, uint32_t va, f32x16_t (&nxt)[kB],
+                                                   const f32x16_t (&cur)[kB], RowState<kD>& st, float top, float c,
+                                                   u32x4_t (&p)[2 * kB], bf16x8_t (&k)[2][kB],
+                                                   bf16x8_t (&v)[2][kD / 32], const Loads& loads) {
+  constexpr int kN = 256 * kB / kD;
+  if constexpr (kT < kD / 16) {
+    if constexpr (kT + 1 < kD / 16) read_k<kD, kB>(sK, ka, kT + 1, k[(kT + 1) & 1]);
+    else read_v<kD>(sV, va, 0, v[0]);
+#pragma unroll
+    for (int b = 0; b < kB; ++b)
+      nxt[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[kT & 1][b], q[kT], kT == 0 ? f32x16_t{} : nxt[b], 0, 0, 0);
+    if constexpr (kT == 0) {
+      __builtin_amdgcn_sched_barrier(0);
+      move_max<kD>(st, top, c);   // beside the first scores
     }
+    if constexpr (kT % 2 == 0) loads.part(kT / 2);
+    weights<kD, kB, kT * kN, kN>(cur, st, c, p);
+    __builtin_amdgcn_sched_barrier(0);
+    scores_and_weights<kD, kB, kT + 1>(sK, sV, q, ka, va, nxt, cur, st, top, c, p, k, v, loads);
+  }
+}
+
+// The products of the current tile beside the maximum of the next one's scores.
+template <int kD, int kB, int kT = 0>
+__device__ __forceinline__ void products_and_top(const uint8_t* sV, uint32_t va, const u32x4_t (&p)[2 * kB],
+                                                 RowState<kD>& st, const f32x16_t (&nxt)[kB], float& top,
+                                                 bf16x8_t (&v)[2][kD / 32]) {
+  if constexpr (kT < 2 * kB) {
+    if constexpr (kT + 1 < 2 * kB) read_v<kD>(sV, va, kT + 1, v[(kT + 1) & 1]);
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int b = 0; b < kD / 32; ++b) {
-      const uint8_t* at = sV + va[b] + t * 16 * kD * 2;
-      const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(at));
-      const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(at + 8 * kD * 2));
-      const auto v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-      st.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v), p[t], st.o[b], 0, 0, 0);
-    }
+    for (int b = 0; b < kD / 32; ++b)
+      st.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[kT & 1][b], __builtin_bit_cast(bf16x8_t, p[kT]), st.o[b], 0, 0, 0);
+    top = top_score<kB>(nxt, kT * (8 / kB), 8 / kB, top);
+    __builtin_amdgcn_sched_barrier(0);
+    products_and_top<kD, kB, kT + 1>(sV, va, p, st, nxt, top, v);
+  }
 }
 
 // Zero the non-finite values of a V tile in LDS.
-template <int kD, int kW>
+template <int kD, int kW, int kKeys>
 __device__ __forceinline__ void zero_nonfinite(uint8_t* sV) {
   uint32_t* w = reinterpret_cast<uint32_t*>(sV);
   for (int i = threadIdx.x; i < kKeys * kD / 2; i += 64 * kW) {
@@ -286,55 +362,61 @@ __device__ __forceinline__ bool plain_row(const PromptArgs& a, int64_t t, int h,
   return true;
 }
 
-template <int kD, int kW>
-__global__ void __launch_bounds__(64 * kW, 2) attn_prompt_kernel(PromptArgs a) {
-  constexpr int kTileBytes = kKeys * kD * 2, kRows = 32 * kW;
-  __shared__ __attribute__((aligned(1024))) uint8_t sK0[kTileBytes], sK1[kTileBytes], sV0[kTileBytes], sV1[kTileBytes];
-  const int lane = threadIdx.x & 63, half = lane >> 5, w = wave_id();
+// The workgroup's barrier, after this wave's LDS reads; loads in flight stay there.
+__device__ __forceinline__ void block_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// kS: key groups.  A workgroup's eight waves are 8 / kS row groups times kS key groups; each key group computes its part
+// of every tile for the workgroup's 256 / kS rows, and the parts are joined at the end.
+template <int kD, int kS>
+__global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
+  constexpr int kW = 8, kRowWaves = kW / kS, kRows = 32 * kRowWaves;
+  constexpr int kB = kS == 4 ? 1 : 2;             // 32-key blocks of a wave's part of a tile
+  constexpr int kPart = 32 * kB, kKeys = kPart * kS;
+  constexpr int kRing = kS == 1 ? 4 : 2;          // stages of a tile of keys, and of values
+  constexpr int kTileBytes = kKeys * kD * 2, kExtra = kRing == 4 ? kTileBytes : 16;
+  // distinct objects, so that the compiler knows that a DMA into one is not read through another
+  __shared__ __attribute__((aligned(1024))) uint8_t sK0[kTileBytes], sK1[kTileBytes], sK2[kExtra], sK3[kExtra];
+  __shared__ __attribute__((aligned(1024))) uint8_t sV0[kTileBytes], sV1[kTileBytes], sV2[kExtra], sV3[kExtra];
+  __shared__ float sM[kW][32], sL[kW][32];
+  const int lane = threadIdx.x & 63, half = lane >> 5, w = wave_id(), rw = w % kRowWaves, kg = w / kRowWaves;
   const int G = a.Hq / a.Hkv, hk = blockIdx.x % a.Hkv;
   const Tile1 t = find_tile(a, blockIdx.x / a.Hkv, G, kRows);
   if (t.seq < 0) return;
   const int rows = t.Lq * G, r0 = t.tile * kRows;
-  const int row = r0 + w * 32 + (lane & 31);
+  const int w_first = r0 + rw * 32, row = w_first + (lane & 31);
   const bool valid = row < rows;
   const int token = row / G, head = hk * G + row % G;
   auto limit_of = [&](int tok) { return a.causal ? min(max(t.Lk - t.Lq + tok + 1, 0), t.Lk) : t.Lk; };
   const int my_seen = valid ? limit_of(token) : 0;
-  // keys the workgroup's last row, this wave's last row and its first row see
-  const int wg_keys = limit_of((min(r0 + kRows, rows) - 1) / G);
-  const int w_first = r0 + w * 32, w_last = min(w_first + 32, rows) - 1;
-  const int w_keys = __builtin_amdgcn_readfirstlane(w_first < rows ? limit_of(w_last / G) : 0);
-  const int w_all = __builtin_amdgcn_readfirstlane(w_first < rows ? limit_of(w_first / G) : 0);
+  const int wg_keys = limit_of((min(r0 + kRows, rows) - 1) / G);   // what the workgroup's last row sees
+  const int w_all = uniform(w_first < rows ? limit_of(w_first / G) : 0);   // what all rows of this wave see
   const int tiles = (wg_keys + kKeys - 1) / kKeys;
 
-  // exponent of a weight per unit of score; a negative scale's sign goes to q, scale 0 to a factor that rounds away
-  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+  const float c = weight_exponent(a.scale);
   bf16x8_t q[kD / 16];
   {
     const uint16_t* p = a.q + (t.q0 + token) * a.q_token + head * a.q_head + 8 * half;
-    const u32x4_t flip = a.scale < 0.f ? u32x4_t{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u} : u32x4_t{0, 0, 0, 0};
+    const uint32_t sign = query_sign(a.scale);
 #pragma unroll
     for (int i = 0; i < kD / 16; ++i) {
       u32x4_t v = {0, 0, 0, 0};
       if (valid) v = *reinterpret_cast<const u32x4_t*>(p + 16 * i);
-      q[i] = __builtin_bit_cast(bf16x8_t, v ^ flip);
+      q[i] = __builtin_bit_cast(bf16x8_t, v ^ u32x4_t{sign, sign, sign, sign});
     }
   }
-  uint32_t ka[kD / 16], va[kD / 32];
-#pragma unroll
-  for (int i = 0; i < kD / 16; ++i)
-    ka[i] = (uint32_t)((lane & 31) * kD * 2 + (((2 * i + half) ^ k_swz<kD>(lane & 31)) << 4));
-#pragma unroll
-  for (int b = 0; b < kD / 32; ++b) {
-    const int key = 4 * half + ((lane & 15) >> 2), chunk = 4 * b + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-    va[b] = (uint32_t)(key * kD * 2 + ((chunk ^ v_swz<kD>(key)) << 4) + (lane & 1) * 8);
-  }
-  TileDma<kD, kW, false> kd;
-  TileDma<kD, kW, true> vd;
+  // this lane's first chunk of a K row and of a V row in LDS; product step t of the scores lies 2 t chunks on, column block
+  // b of V 4 b chunks on, both under the swizzle, so that one xor moves there
+  const uint32_t ka0 = (uint32_t)((lane & 31) * kD * 2 + ((half ^ k_swz<kD>(lane & 31)) << 4));
+  const int vkey = 4 * half + ((lane & 15) >> 2);
+  const uint32_t va0 = (uint32_t)(vkey * kD * 2 + (((((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) ^ v_swz<kD>(vkey)) << 4) + (lane & 1) * 8);
+  const uint32_t part = (uint32_t)(kg * kPart * kD * 2);   // this wave's part of a tile
+  TileDma<kD, kW, kKeys, false> kd;
+  TileDma<kD, kW, kKeys, true> vd;
   kd.init(a.k + t.k0 * a.k_token + hk * a.k_head, a.k_token, t.Lk);
   vd.init(a.v + t.k0 * a.v_token + hk * a.v_head, a.v_token, t.Lk);
 
   RowState<kD> st;
+  constexpr int kL = TileDma<kD, kW, kKeys, false>::kLoads;   // DMA loads of a tile of keys or values per wave
   auto pass = [&](bool again) {
 #pragma unroll
     for (int b = 0; b < kD / 32; ++b)
@@ -345,29 +427,120 @@ __global__ void __launch_bounds__(64 * kW, 2) attn_prompt_kernel(PromptArgs a) {
     st.l = st.mc = 0.f;
     if (tiles == 0) return;
     kd.issue(sK0, 0);
+    kd.issue(sK1, kKeys);
     vd.issue(sV0, 0);
-    auto step = [&](int j, const uint8_t* cK, uint8_t* cV, uint8_t* nK, uint8_t* nV) {
-      wait_dma();          // tile j has landed (this wave's loads), and for every wave after the barrier,
-      __syncthreads();     // which also ends all reads of the other stage
+    if constexpr (kRing == 4) {
+      kd.issue(sK2, 2 * kKeys);
+      vd.issue(sV1, kKeys);
+    }
+    wait_vm<(kRing == 4 ? 4 : 2) * kL>();   // all but the first tile of keys may still be on their way
+    block_barrier();
+    f32x16_t s0[kB], s1[kB];
+    const int mine = kg * kPart;                // first key of this wave's part of tile 0
+    scores<kD, kB>(sK0 + part, q, ka0, s0);
+    if (mine + kPart > w_all) mask_scores<kB>(s0, my_seen - mine);
+    float top = top_score<kB>(s0, 0, 16, -INFINITY);   // of the tile whose weights come next
+    // Step j: the scores of tile j + 1 (in K1) beside the weights of tile j, then its products (with V0) beside the next
+    // maximum.  The next tiles to load (keys j + 3 and values j + 2, or j + 2 and j + 1) go to Kn and Vn.
+    auto step = [&](int j, f32x16_t (&cur)[kB], f32x16_t (&nxt)[kB], const uint8_t* K1, uint8_t* Kn, uint8_t* V0, uint8_t* Vn) {
       const int j0 = j * kKeys;
-      if (j + 1 < tiles) {
-        kd.issue(nK, j0 + kKeys);
-        vd.issue(nV, j0 + kKeys);
-      }
+      const NextTiles<kD, kW, kKeys> loads{kd, vd, kd.at(j0 + (kRing == 4 ? 3 : 2) * kKeys), vd.at(j0 + kRing / 2 * kKeys), Kn, Vn};
       if (again) {
-        zero_nonfinite<kD, kW>(cV);
+        zero_nonfinite<kD, kW, kKeys>(V0);
         __syncthreads();
       }
-      if (j0 < w_keys) tile_step<kD>(cK, cV, q, st, ka, va, c, j0 + kKeys > w_all, my_seen - j0);
+      u32x4_t p[2 * kB];
+      bf16x8_t k[2][kB], v[2][kD / 32];
+      uint32_t ka = ka0, va = va0;
+      asm volatile("" : "+v"(ka), "+v"(va));   // the xors stay here: twelve addresses kept over the loop would spill
+      read_k<kD, kB>(K1 + part, ka, 0, k[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      // (past the last tile: zeros' scores, not used)
+      scores_and_weights<kD, kB>(K1 + part, V0 + part, q, ka, va, nxt, cur, st, top, c, p, k, v, loads);
+      const int next = j0 + kKeys + mine;
+      if (next + kPart > w_all) mask_scores<kB>(nxt, my_seen - next);
+      __builtin_amdgcn_sched_barrier(0);
+      top = -INFINITY;
+      products_and_top<kD, kB>(V0 + part, va, p, st, nxt, top, v);
+    };
+    // Before a step, K of the next tile and V of this one have landed: this wave's loads, and every wave's after the
+    // barrier, which also ends all reads of the stages that are loaded next.  With four stages one barrier serves two
+    // steps, which lets the two waves of a SIMD drift apart: one's weights then run beside the other's products.
+    auto sync = [&] {
+      wait_vm<0>();
+      block_barrier();
     };
     for (int j = 0;;) {
-      step(j, sK0, sV0, sK1, sV1);
-      if (++j == tiles) break;
-      step(j, sK1, sV1, sK0, sV0);
-      if (++j == tiles) break;
+      sync();
+      if constexpr (kRing == 4) {
+        step(j, s0, s1, sK1, sK3, sV0, sV2);
+        if (++j == tiles) break;
+        step(j, s1, s0, sK2, sK0, sV1, sV3);
+        if (++j == tiles) break;
+        sync();
+        step(j, s0, s1, sK3, sK1, sV2, sV0);
+        if (++j == tiles) break;
+        step(j, s1, s0, sK0, sK2, sV3, sV1);
+        if (++j == tiles) break;
+      } else {
+        step(j, s0, s1, sK1, sK0, sV0, sV1);
+        if (++j == tiles) break;
+        sync();
+        step(j, s1, s0, sK0, sK1, sV1, sV0);
+        if (++j == tiles) break;
+      }
+    }
+    wait_vm<0>();   // no load may land in the stages after this
+  };
+  // The key groups' parts of each row, brought to their common maximum and added: key group 0 holds the row.
+  auto join = [&] {
+    if constexpr (kS > 1) {
+      st.l += other_half(st.l);
+      const float own = st.m == -INFINITY ? -INFINITY : st.mc;
+      __syncthreads();                    // all reads of the stages are done
+      sM[w][lane & 31] = own;
+      __syncthreads();
+      float m = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < kS; ++g) m = fmaxf(m, sM[g * kRowWaves + rw][lane & 31]);
+      const float f = own == -INFINITY ? (st.l == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(own - m);
+      st.mc = m == -INFINITY ? 0.f : m;
+      st.l *= f;
+#pragma unroll
+      for (int b = 0; b < kD / 32; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) st.o[b][r] *= f;
+#pragma unroll
+      for (int n = kS / 2; n >= 1; n /= 2) {   // groups n .. 2 n - 1 go to groups 0 .. n - 1
+        const int at = kg % n * kRowWaves + rw;
+        f32x4_t* box = reinterpret_cast<f32x4_t*>(at == 0 ? sK0 : at == 1 ? sK1 : at == 2 ? sV0 : sV1) + lane;
+        if (kg >= n && kg < 2 * n) {
+#pragma unroll
+          for (int b = 0; b < kD / 32; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+              box[(4 * b + r / 4) * 64] = f32x4_t{st.o[b][r], st.o[b][r + 1], st.o[b][r + 2], st.o[b][r + 3]};
+          sL[at][lane & 31] = st.l;
+        }
+        __syncthreads();
+        if (kg < n) {
+#pragma unroll
+          for (int b = 0; b < kD / 32; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+              const f32x4_t x = box[(4 * b + r / 4) * 64];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st.o[b][r + i] += x[i];
+            }
+          st.l += sL[at][lane & 31];
+        }
+        __syncthreads();
+      }
+      st.l = half == 0 ? st.l : 0.f;      // the halves are added once more below
     }
   };
   pass(false);
+  join();
   auto non_finite = [&] {
     float top = 0.f;
 #pragma unroll
@@ -375,13 +548,14 @@ __global__ void __launch_bounds__(64 * kW, 2) attn_prompt_kernel(PromptArgs a) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = abs_max(top, st.o[b][r]);
     top = abs_max(top, other_half(top));
-    return valid && !(top < INFINITY);
+    return valid && kg == 0 && !(top < INFINITY);
   };
   const bool bad = non_finite();
-  bool done = !valid;
+  bool done = !valid || kg > 0;
   if (__syncthreads_or(bad)) {
     __syncthreads();
     pass(true);
+    join();
     // rows that were not finite: by plain loops, kept where the row itself sees such a value
     uint64_t todo = __ballot(bad) & 0xFFFFFFFFull;
     while (todo) {
@@ -405,10 +579,8 @@ __global__ void __launch_bounds__(64 * kW, 2) attn_prompt_kernel(PromptArgs a) {
       uint32_t x[2], y[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
-            f32x2_t{st.o[b][4 * g + 2 * i] * inv, st.o[b][4 * g + 2 * i + 1] * inv}, bf16x2_t));
-        y[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
-            f32x2_t{st.o[b][4 * g + 4 + 2 * i] * inv, st.o[b][4 * g + 4 + 2 * i + 1] * inv}, bf16x2_t));
+        x[i] = pack_bf16(st.o[b][4 * g + 2 * i] * inv, st.o[b][4 * g + 2 * i + 1] * inv);
+        y[i] = pack_bf16(st.o[b][4 * g + 4 + 2 * i] * inv, st.o[b][4 * g + 4 + 2 * i + 1] * inv);
       }
       const auto e0 = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
       const auto e1 = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
@@ -416,18 +588,30 @@ __global__ void __launch_bounds__(64 * kW, 2) attn_prompt_kernel(PromptArgs a) {
     }
 }
 
-template <int kD, int kW>
+template <int kD, int kS>
 hipError_t launch(const PromptArgs& a, hipStream_t stream) {
   // at most one ragged tile for each sequence; workgroups past the last tile exit at once
-  const int64_t tiles = a.total_q * (a.Hq / a.Hkv) / (32 * kW) + min((int64_t)a.n_seqs, a.total_q);
-  attn_prompt_kernel<kD, kW><<<dim3((unsigned)(tiles * a.Hkv)), dim3(64 * kW), 0, stream>>>(a);
+  const int64_t tiles = a.total_q * (a.Hq / a.Hkv) / (256 / kS) + min((int64_t)a.n_seqs, a.total_q);
+  attn_prompt_kernel<kD, kS><<<dim3((unsigned)(tiles * a.Hkv)), dim3(512), 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <int kD>
+hipError_t launch_dim(const PromptArgs& a, hipStream_t stream) {
+  // Tiles of 256 rows, against 256 CUs of one workgroup each: where they do not fill the chip, the keys are split over a
+  // workgroup's waves instead of more rows.  Measured, one causal prompt of 8 query heads and 1 key head, D 128
+  // (us at 1 / 2 / 4 key groups): 2048 tokens (64 tiles) 56 / 37 / 30, 4096 (128) 102 / 65 / 65, 8192 (256) 201 / 155 / 202,
+  // 12000 (375) 329 / 332 / 399, 16384 (512) 558 / 573 / 702; 16 prompts of 1 to 1500 tokens (134) 53 / 34 / 46.
+  const int64_t tiles = a.total_q * a.Hq / 256;
+  if (tiles >= 320) return launch<kD, 1>(a, stream);
+  if (tiles >= 96) return launch<kD, 2>(a, stream);
+  return launch<kD, 4>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_attn_prompt(const PromptArgs& a, hipStream_t stream) {
-  return a.D == 64 ? launch<64, 8>(a, stream) : launch<128, 8>(a, stream);
+  return a.D == 64 ? launch_dim<64>(a, stream) : launch_dim<128>(a, stream);
 }
 
 }  // namespace sgt

@@ -292,6 +292,23 @@ def test_prompt_pieces_and_empty_rows(nq, nk, causal):
         check_prompt(q, k, v, nq, nk, causal)
 
 
+@pytest.mark.parametrize("hq,hkv", [(176, 22), (448, 56), (450, 50)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_many_rows(hq, hkv, d):
+    """Enough rows to fill the GPU: the keys are split over fewer and fewer of a workgroup's waves."""
+    rng = np.random.default_rng(hq)
+    nq, nk = [130, 0, 1, 169], [130, 5, 40, 169]
+    q, k, v = make_prompt(rng, nq, nk, hq, hkv, d)
+    clean, clean_lse = check_prompt(q, k, v, nq, nk)
+    k2, v2 = k.clone(), v.clone()
+    k2[60], v2[60] = NAN, INF                  # seen by queries 60 .. 129 of the first sequence
+    out, lse = torch.empty_like(clean), torch.empty_like(clean_lse)
+    sgt.attn_prompt(q, k2, v2, out, cu(nq), cu(nk), lse=lse)
+    ok = torch.ones(300, dtype=torch.bool, device=DEV)
+    ok[60:130] = False
+    assert torch.equal(out[ok], clean[ok]) and torch.equal(lse[ok], clean_lse[ok]) and torch.isnan(out[~ok].float()).all()
+
+
 def test_prompt_large_scores_and_scale():
     rng = np.random.default_rng(4)
     n = [150, 90]
