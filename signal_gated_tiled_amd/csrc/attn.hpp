@@ -29,6 +29,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
+// The two values of a packed pair.
+__device__ __forceinline__ float low_bf16(uint32_t two) { return __uint_as_float(two << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t two) { return __uint_as_float(two & 0xFFFF0000u); }
+
 // A value that all lanes share, in scalar registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform(int64_t v) {

@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
             *reinterpret_cast<u32x4_t*>(st.v + x * 1024 + lane * 16) = u32x4_t{0, 0, 0, 0};
         __builtin_amdgcn_wave_barrier();
       }
-      s16x4_t p[kNQ][kS];
+      // weights in two bf16 parts: the second holds what the first's rounding leaves, and its products are free here
+      s16x4_t p[kNQ][kS], p2[kNQ][kS];
 #pragma unroll
       for (int i = 0; i < kNQ; ++i) {
         float t = s[i][0][0];
@@ -268,9 +269,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
             const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][h][j], c2, -mc[i]));
             const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][h][j + 1], c2, -mc[i]));
             l[i] += e0 + e1;
-            const auto two = __builtin_bit_cast(s16x2_t, __builtin_convertvector(f32x2_t{e0, e1}, bf16x2_t));
+            const uint32_t hi = pack_bf16(e0, e1);
+            const auto two = __builtin_bit_cast(s16x2_t, hi);
+            const auto rest = __builtin_bit_cast(s16x2_t, pack_bf16(e0 - low_bf16(hi), e1 - high_bf16(hi)));
             p[i][h][j] = two[0];
             p[i][h][j + 1] = two[1];
+            p2[i][h][j] = rest[0];
+            p2[i][h][j + 1] = rest[1];
           }
       }
       const int key = 4 * g + (col >> 2), at0 = key * kD * 2 + ((((lane & 3) >> 1) ^ v_swz<kD>(key)) << 4) + (lane & 1) * 8;
@@ -280,7 +285,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
         for (int n = 0; n < kNB; ++n) {   // chunks 2 n and 2 n + 1
           const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(st.v + 16 * h * kD * 2 + (at0 ^ (n << 5))));
 #pragma unroll
-          for (int i = 0; i < kNQ; ++i) o[i][n] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, p[i][h], o[i][n], 0, 0, 0);
+          for (int i = 0; i < kNQ; ++i) {
+            o[i][n] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, p[i][h], o[i][n], 0, 0, 0);
+            o[i][n] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(v, p2[i][h], o[i][n], 0, 0, 0);
+          }
         }
       // every read of the stage has returned before the next DMA into it
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -236,8 +236,9 @@ __device__ __forceinline__ void move_max(RowState<kD>& st, float top, float c) {
 }
 
 // Weights of elements [kAt, kAt + kN) of a tile's 16 kB per lane; product step t covers keys 16 t .. 16 t + 15.
+// With one block per tile they come in two bf16 parts, the second (steps 2 and 3) of what the first's rounding leaves.
 template <int kD, int kB, int kAt, int kN>
-__device__ __forceinline__ void weights(const f32x16_t (&s)[kB], RowState<kD>& st, float c, u32x4_t (&p)[2 * kB]) {
+__device__ __forceinline__ void weights(const f32x16_t (&s)[kB], RowState<kD>& st, float c, u32x4_t (&p)[4]) {
 #pragma unroll
   for (int i = kAt; i < kAt + kN; i += 2) {
     const int b = i / 16, r = i % 16;
@@ -247,6 +248,7 @@ __device__ __forceinline__ void weights(const f32x16_t (&s)[kB], RowState<kD>& s
     uint32_t two = pack_bf16(e0, e1);
     asm volatile("" : "+v"(two));   // computed here, beside the next scores, and not where it is first used
     p[i / 8][i % 8 / 2] = two;
+    if constexpr (kB == 1) p[2 + i / 8][i % 8 / 2] = pack_bf16(e0 - low_bf16(two), e1 - high_bf16(two));
   }
   asm volatile("" : "+v"(st.l));   // summed here, or the weights would stay in registers until they are
 }
@@ -277,7 +279,7 @@ template <int kD, int kB, int kT = 0, class Loads>
 __device__ __forceinline__ void scores_and_weights(const uint8_t* sK, const uint8_t* sV, const bf16x8_t (&q)[kD / 16],
                                                    uint32_t ka, uint32_t va, f32x16_t (&nxt)[kB],
                                                    const f32x16_t (&cur)[kB], RowState<kD>& st, float top, float c,
-                                                   u32x4_t (&p)[2 * kB], bf16x8_t (&k)[2][kB],
+                                                   u32x4_t (&p)[4], bf16x8_t (&k)[2][kB],
                                                    bf16x8_t (&v)[2][kD / 32], const Loads& loads) {
   constexpr int kN = 256 * kB / kD;
   if constexpr (kT < kD / 16) {
@@ -299,14 +301,16 @@ __device__ __forceinline__ void scores_and_weights(const uint8_t* sK, const uint
 
 // The products of the current tile beside the maximum of the next one's scores.
 template <int kD, int kB, int kT = 0>
-__device__ __forceinline__ void products_and_top(const uint8_t* sV, uint32_t va, const u32x4_t (&p)[2 * kB],
+__device__ __forceinline__ void products_and_top(const uint8_t* sV, uint32_t va, const u32x4_t (&p)[4],
                                                  RowState<kD>& st, const f32x16_t (&nxt)[kB], float& top,
                                                  bf16x8_t (&v)[2][kD / 32]) {
   if constexpr (kT < 2 * kB) {
     if constexpr (kT + 1 < 2 * kB) read_v<kD>(sV, va, kT + 1, v[(kT + 1) & 1]);
 #pragma unroll
-    for (int b = 0; b < kD / 32; ++b)
-      st.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[kT & 1][b], __builtin_bit_cast(bf16x8_t, p[kT]), st.o[b], 0, 0, 0);
+    for (int x = kT; x < 4; x += 2 * kB)   // the weights' second part too, where there is one
+#pragma unroll
+      for (int b = 0; b < kD / 32; ++b)
+        st.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[kT & 1][b], __builtin_bit_cast(bf16x8_t, p[x]), st.o[b], 0, 0, 0);
     top = top_score<kB>(nxt, kT * (8 / kB), 8 / kB, top);
     __builtin_amdgcn_sched_barrier(0);
     products_and_top<kD, kB, kT + 1>(sV, va, p, st, nxt, top, v);
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
         zero_nonfinite<kD, kW, kKeys>(V0);
         __syncthreads();
       }
-      u32x4_t p[2 * kB];
+      u32x4_t p[4];
       bf16x8_t k[2][kB], v[2][kD / 32];
       uint32_t ka = ka0, va = va0;
       asm volatile("" : "+v"(ka), "+v"(va));   // the xors stay here: twelve addresses kept over the loop would spill
