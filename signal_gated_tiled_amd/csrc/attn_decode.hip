@@ -62,6 +62,11 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int64_t room
   return (int)max((n + kT - 1) / kT, (int64_t)1);   // an empty sequence is one tile of unseen keys
 }
 
+// x / y of values that rarely need their upper halves.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return ((uint64_t)(x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // Inclusive prefix sum over the workgroup and its total; `red` holds kWaves words.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -113,12 +118,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   const int64_t room = (int64_t)a.max_pages * a.page_size;
 
   // this workgroup's range of the units (of each problem its tiles, then its cost)
-  int64_t total = 0;
-  int top = 0;
+  int64_t total = 0, end0 = 0, total0 = 0;   // end0, total0: of the first kThreads sequences
+  int top = 0, cost0 = 0;
   for (int c = 0; c < a.B; c += kThreads) {
-    const int n = tiles_of<kT>(a, c + tid, room);
+    const int n = tiles_of<kT>(a, c + tid, room), cost = n > 0 ? n + kProblemCost : 0;
     int64_t t;
-    block_scan(n > 0 ? n + kProblemCost : 0, red, &t);
+    const int64_t end = block_scan(cost, red, &t);
+    if (c == 0) {
+      end0 = end;
+      total0 = t;
+      cost0 = cost;
+    }
     total += t;
     top = max(top, n);
   }
@@ -132,15 +142,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   top = uniform(top);
   const int64_t units = uniform(total) * HC;
   const int64_t grid = gridDim.x;
-  const int64_t chunk = max(max((units + grid - 1) / grid, (int64_t)kMinTiles), (int64_t)(top + kMaxParts - 1) / kMaxParts);
+  const int64_t chunk = max(max(quotient(units + grid - 1, grid), (int64_t)kMinTiles), (int64_t)((top + kMaxParts - 1) / kMaxParts));
   const int64_t u0 = blockIdx.x * chunk, u1 = min(u0 + chunk, units);
   if (u0 >= units) return;
   for (int64_t c = 0, before = 0; c < a.B; c += kThreads) {
-    const int n = tiles_of<kT>(a, (int)c + tid, room);
-    int64_t t;
-    const int cost = n > 0 ? n + kProblemCost : 0;
-    const int64_t end = before + block_scan(cost, red, &t);
-    if (n > 0 && (end - cost) * HC <= u0 && u0 < end * HC) {
+    int64_t end = end0, t = total0;
+    int cost = cost0;
+    if (c > 0) {
+      const int n = tiles_of<kT>(a, (int)c + tid, room);
+      cost = n > 0 ? n + kProblemCost : 0;
+      end = block_scan(cost, red, &t);
+    }
+    end += before;
+    if (cost > 0 && (end - cost) * HC <= u0 && u0 < end * HC) {
       found[0] = c + tid;
       found[1] = end - cost;
     }
@@ -151,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   int b = uniform((int)found[0]);
   int64_t start = uniform(found[1]) * HC;   // first unit of the problem
   int n_tiles = tiles_of<kT>(a, b, room);
-  int hc = (int)((u0 - start) / (n_tiles + kProblemCost));
+  int hc = (int)quotient(u0 - start, n_tiles + kProblemCost);
   start += (int64_t)hc * (n_tiles + kProblemCost);
 
   const float c2 = weight_exponent(a.scale);
@@ -333,8 +347,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
     // join the waves: each scales its output to the common maximum and leaves it in its stage
     const int jl = fresh_lane(), jt = w * 64 + jl, jg = jl >> 4, jc = jl & 15;
     const bool whole = ta == 0 && tb == n_tiles;
-    const int64_t w_first = start / chunk;
-    const int64_t slot = blockIdx.x * 2 + (blockIdx.x == w_first && start % chunk ? 1 : 0);
+    const int64_t w_first = quotient(start, chunk);
+    const bool inside = start != w_first * chunk;   // the problem starts inside a range: that part has the second slot
+    const int64_t slot = blockIdx.x * 2 + (blockIdx.x == w_first && inside ? 1 : 0);
     float* part = parts + slot * kSlotFloats;
     const __amdgpu_buffer_rsrc_t rp = make_rsrc(part, kSlotFloats * 4);
 #pragma unroll
@@ -394,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
     if (!whole) {
       // the parts went to the device's coherence point; once every wave's stores are acknowledged this workgroup counts
       // itself in, and the last one of the problem joins all parts in order
-      const int64_t w_last = (start + n_tiles - 1) / chunk;
+      const int64_t w_last = quotient(start + n_tiles - 1, chunk);
       const int n_parts = (int)(w_last - w_first) + 1;
       uint32_t* counter = counters + (int64_t)b * HC + hc;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -407,28 +422,41 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       __syncthreads();
       if (last) {
         acquire_agent();
-        const int64_t s_first = w_first * 2 + (start % chunk ? 1 : 0);   // later parts lie in their workgroup's first slot
+        const int64_t s_first = w_first * 2 + (inside ? 1 : 0);   // later parts lie in their workgroup's first slot
         const __amdgpu_buffer_rsrc_t ra = make_rsrc(parts, (uint64_t)kGrid * 2 * kSlotFloats * 4);
         for (int e = jt; e < nh * kD / 4; e += kThreads) {
           const int r = e / (kD / 4), at = e % (kD / 4);
           auto off = [&](int i, int f) {
             return (uint32_t)(((i == 0 ? s_first : (w_first + i) * 2) * kSlotFloats + f) * 4);
           };
-          auto word = [&](int i, int f) {
-            return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, off(i, f), 0, kCpolSc1));
-          };
-          float M = -INFINITY;
-#pragma unroll 4
-          for (int i = 0; i < n_parts; ++i) M = fmaxf(M, word(i, kMaxRows * 128 + r));
-          float L = 0.f;
+          float M = -INFINITY, L = 0.f;
           f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-          for (int i = 0; i < n_parts; ++i) {
-            const float mi = word(i, kMaxRows * 128 + r), li = word(i, kMaxRows * 129 + r);
-            const f32x4_t x = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, off(i, r * kD + 4 * at), 0, kCpolSc1));
-            const float f = mi == -INFINITY ? (li == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mi - M);
-            L += li * f;
-            v += x * f;
+          constexpr int kAtOnce = 16;   // parts whose loads are in flight together
+          for (int i0 = 0; i0 < n_parts; i0 += kAtOnce) {
+            float mi[kAtOnce], li[kAtOnce];
+            f32x4_t xi[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const int i = min(i0 + u, n_parts - 1);
+              mi[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, off(i, kMaxRows * 128 + r), 0, kCpolSc1));
+              li[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, off(i, kMaxRows * 129 + r), 0, kCpolSc1));
+              xi[u] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, off(i, r * kD + 4 * at), 0, kCpolSc1));
+            }
+            float Mn = M;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) Mn = fmaxf(Mn, mi[u]);
+            const float f0 = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(M - Mn);
+            M = Mn;
+            L *= f0;
+            v *= f0;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const float f = mi[u] == -INFINITY ? (li[u] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mi[u] - M);
+              if (i0 + u < n_parts) {
+                L += li[u] * f;
+                v += xi[u] * f;
+              }
+            }
           }
           const float inv = 1.f / L;
           v = L == 0.f ? f32x4_t{0.f, 0.f, 0.f, 0.f} : v * inv;
