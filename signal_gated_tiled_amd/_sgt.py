@@ -312,6 +312,28 @@ def gemm_rs_static_scratch_bytes() -> int:
     return int(lib().sgt_gemm_rs_static_scratch_bytes())
 
 
+_torch_module = None
+
+
+def _torch():
+    """The torch module, imported on the first call (an import statement in each call would cost more than its checks)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _code(dtype) -> int:
+    """SGT_BF16 or SGT_F32 of a torch dtype."""
+    torch = _torch()
+    if dtype is torch.bfloat16:
+        return SGT_BF16
+    if dtype is torch.float32:
+        return SGT_F32
+    raise TypeError("tensors must be bfloat16 or float32, got %s" % dtype)
+
+
 def _layer_ptr(t, name: str, dtype, shape, device: int) -> int:
     """Device pointer of a dense tensor of this dtype and shape on GPU `device`; None is NULL."""
     if t is None:
@@ -329,11 +351,11 @@ def _layer_ptr(t, name: str, dtype, shape, device: int) -> int:
 
 def _current_device(t, name: str) -> int:
     """The GPU of `t`, which must be the calling thread's current one (the layer operators run there)."""
-    import torch
     dev = t.get_device()
     if dev < 0:
         raise ValueError("%s must be a GPU tensor" % name)
-    if torch.cuda.current_device() != dev:
+    torch = _torch()
+    if torch._C._cuda_getDevice() != dev:
         raise ValueError("the call runs on the current device (%d); %s is on %s" %
                          (torch.cuda.current_device(), name, t.device))
     return dev
@@ -341,8 +363,7 @@ def _current_device(t, name: str) -> int:
 
 def _layer_stream(stream, device: int) -> int:
     """Raw handle of `stream`, or of the device's current stream (without building a stream object for it)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: float = 1e-6, stream=None):
@@ -350,7 +371,7 @@ def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: f
     eps) * weight.  x: T x H fp32 or bf16, rows may be strided; weight: H; residual, sum_out: T x H of one dtype, either
     may be None; out: T x H bf16, fp32 or float8_e4m3fn, the last with fp32 scales: T x 1 (one per row) or
     T x ceil(H / 128) (one per 128 columns)."""
-    import torch
+    torch = _torch()
     dev = _current_device(x, "x")
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be T x H with contiguous rows")
@@ -363,12 +384,12 @@ def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: f
         out_code, block = SGT_F8E4M3, 0 if scales.shape[1] == 1 else 128
         s_shape = (T, 1 if block == 0 else -(-H // 128))
     else:
-        out_code, block, s_shape = _dtype_code(out), 0, None
-    _check(lib().sgt_rms_norm(x.data_ptr(), _dtype_code(x), x.stride(0) if T > 1 else max(H, 1),
+        out_code, block, s_shape = _code(out.dtype), 0, None
+    _check(lib().sgt_rms_norm(x.data_ptr(), _code(x.dtype), x.stride(0) if T > 1 else max(H, 1),
                               _layer_ptr(residual, "residual", r_type, (T, H), dev),
                               _layer_ptr(sum_out, "sum_out", r_type, (T, H), dev),
                               SGT_BF16 if r_type == torch.bfloat16 else SGT_F32,
-                              _layer_ptr(weight, "weight", weight.dtype, (H,), dev), _dtype_code(weight),
+                              _layer_ptr(weight, "weight", weight.dtype, (H,), dev), _code(weight.dtype),
                               _layer_ptr(out, "out", out.dtype, (T, H), dev), out_code,
                               _layer_ptr(scales, "scales", torch.float32, s_shape, dev), block, T, H, eps,
                               _layer_stream(stream, dev)))
@@ -380,7 +401,7 @@ def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_gro
     int32 and gate: T x k fp32, written, as a2a_dispatch and a2a_combine take them; bias: E fp32, added to the scores
     for the choice only; score: 'softmax' or 'sigmoid'; with n_group > 1 the experts come from the topk_group groups of
     largest sum of their group_top largest scores (with the bias)."""
-    import torch
+    torch = _torch()
     dev = _current_device(logits, "logits")
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be T x E with contiguous rows")
@@ -388,7 +409,7 @@ def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_gro
     k = topk_ids.shape[1]
     if n_group == 1:
         group_top = 1
-    _check(lib().sgt_moe_gate(logits.data_ptr(), _dtype_code(logits), logits.stride(0) if T > 1 else max(E, 1),
+    _check(lib().sgt_moe_gate(logits.data_ptr(), _code(logits.dtype), logits.stride(0) if T > 1 else max(E, 1),
                               _layer_ptr(bias, "bias", torch.float32, (E,), dev),
                               _layer_ptr(topk_ids, "topk_ids", torch.int32, (T, k), dev),
                               _layer_ptr(gate, "gate", torch.float32, (T, k), dev), T, E, k, SCORES[score], n_group,
@@ -397,7 +418,7 @@ def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_gro
 
 def _heads(t, name: str, dev):
     """(pointer, token stride, head stride) of a bf16 tokens x heads x D tensor with contiguous heads."""
-    import torch
+    torch = _torch()
     if t.dtype != torch.bfloat16:
         raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
     if t.get_device() != dev:
@@ -412,7 +433,7 @@ def attn_prompt(q, k, v, out, cu_q, cu_k, *, lse=None, causal: bool = True, scal
     """Attention over packed prompts (sgt_attn_prompt).  q: total_q x Hq x D, k and v: total_k x Hkv x D, bf16, any
     token and head strides (slices of one QKV tensor can be passed); out: total_q x Hq x D bf16; cu_q, cu_k: int32
     offsets of the sequences (n_seqs + 1); lse: total_q x Hq fp32 or None; scale: 1 / sqrt(D) by default."""
-    import torch
+    torch = _torch()
     dev = _current_device(q, "q")
     qp, kp, vp = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
     total_q, Hq, D = q.shape
@@ -441,7 +462,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, workspace, *, l
     strided; k_cache, v_cache: n_pages x page_size x Hkv x D bf16 with the same strides (a transposed view of
     n_pages x Hkv x page_size x D can be passed); block_table: B x max_pages int32, rows may be strided; seq_lens: B
     int32; out: B x Hq x D bf16 or fp32; workspace: at least attn_decode_workspace(B, Hq, Hkv, D) bytes."""
-    import torch
+    torch = _torch()
     dev = _current_device(q, "q")
     q_ptr, q_stride, q_head = _heads(q, "q", dev)
     B, Hq, D = q.shape
@@ -462,7 +483,7 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, workspace, *, l
     _check(lib().sgt_attn_decode(q_ptr, q_stride, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n_pages,
                                  page_size, block_table.data_ptr(), block_table.stride(0) if B > 1 else max_pages,
                                  max_pages, _layer_ptr(seq_lens, "seq_lens", torch.int32, (B,), dev),
-                                 _layer_ptr(out, "out", out.dtype, (B, Hq, D), dev), _dtype_code(out),
+                                 _layer_ptr(out, "out", out.dtype, (B, Hq, D), dev), _code(out.dtype),
                                  _layer_ptr(lse, "lse", torch.float32, (B, Hq), dev),
                                  _layer_ptr(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.numel() * workspace.element_size(),
                                  B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _layer_stream(stream, dev)))

@@ -39,7 +39,7 @@ constexpr int kRing = 4;                      // LDS stages of a wave
 constexpr int kGrid = 256;                   // workgroups: one on each CU (128 KiB of LDS)
 constexpr int kMinTiles = 4;                 // tiles of a range at least: one for each wave
 constexpr int kMaxParts = 64;                // a problem is cut into about this many parts at most
-constexpr int kProblemCost = 16;             // what starting and joining a problem costs a workgroup, in tiles
+constexpr int kProblemCost = 24;             // what starting and joining a problem costs a workgroup, in tiles
 constexpr int kMaxRows = 32;                 // query heads of a chunk
 constexpr int kSlotFloats = kMaxRows * 128 + 2 * kMaxRows;   // one part: outputs, maxima, sums
 

@@ -29,7 +29,7 @@ struct GateArgs {
   int32_t E, k;
   int32_t n_group, topk_group, group_top;
   int32_t sigmoid, renormalize, bf16;
-  int32_t wide;         // rows can be read four logits at a time
+  int32_t wide, wide_bias;   // rows, and the bias, can be read four values at a time
   float scale;
 };
 

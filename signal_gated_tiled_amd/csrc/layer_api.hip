@@ -93,6 +93,7 @@ sgt_status sgt_moe_gate(const void* logits, int dtype, int64_t stride, const flo
   a.n_group = n_group; a.topk_group = topk_group; a.group_top = group_top;
   a.sigmoid = score == SGT_SCORE_SIGMOID; a.renormalize = renormalize != 0; a.bf16 = dtype == SGT_BF16;
   a.wide = stride % 4 == 0 && aligned(logits, 4 * bytes_of(dtype));
+  a.wide_bias = aligned(bias, 16);
   a.scale = scale;
   HIP_TRY(launch_moe_gate(a, static_cast<hipStream_t>(stream)));
   return SGT_OK;

@@ -1,15 +1,16 @@
 // Routing of tokens to experts: softmax or sigmoid scores, a bias that takes
 // part in the choice only, groups of experts, top-k and renormalised weights.
 //
-// The logits are read once and little is written, so the choice itself bounds
-// this: kL lanes hold one token's experts, lane j the kSlots from j kSlots on, and
-// each of the k rounds finds the largest remaining choice value.  A value and its
-// expert are one positive double, made of the value's order-preserving 32-bit key and
-// the expert's number from the end, so that one v_max_f64 per value keeps the
-// larger one and, of equal ones, the lower expert; four of them over DPP exchanges
-// (16 lanes) finish a round for the four tokens of a wave at once.  The chosen
-// experts' scores are computed again from their logits at the end, which costs one
-// small gather instead of carrying every score through the rounds.
+// The logits are read once and little is written, so the choice itself, in vector
+// instructions, bounds this.  kL lanes hold one token's experts, lane j the kSlots
+// from j kSlots on.  A choice value and its expert are one positive double, made of
+// the value's order-preserving 32-bit key and the expert's number from the end, so
+// that one v_max_f64 keeps the larger one and, of equal ones, the lower expert.  Each
+// lane sorts what it holds (a network of maxima and minima; the kTop largest are
+// enough); each of the k rounds then takes the largest of the lanes' heads, by four
+// DPP exchanges (16 lanes) for the four tokens of a wave at once, and the lane that
+// held it moves up.  The chosen experts' scores are computed again from their logits
+// at the end, which costs one small gather instead of carrying every score along.
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
@@ -26,8 +27,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 // Order-preserving map of an fp32 value (not NaN) to uint32; -0 and +0 alike, as comparison has them.
 __device__ __forceinline__ uint32_t order_key(float f) {
-  uint32_t u = __float_as_uint(f);
-  if (u == 0x80000000u) u = 0u;
+  const uint32_t u = __float_as_uint(f + 0.f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
@@ -71,10 +71,87 @@ template <int kL, class T, class F> __device__ __forceinline__ T over_token(T v,
   return v;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + expf(-x)); }
+__device__ __forceinline__ double smaller(double a, double b) {
+  double m;
+  asm("v_min_f64 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
+  return m;
+}
+
+// Descending order of s[at], s[at + step], ... (kN of them): Batcher's odd-even merge sort (1968).
+template <int kM> __device__ __forceinline__ void exchange(double (&s)[kM], int i, int k) {
+  const double a = larger(s[i], s[k]), b = smaller(s[i], s[k]);
+  s[i] = a;
+  s[k] = b;
+}
+template <int kN, int kStep, int kM> __device__ __forceinline__ void merge_sorted(double (&s)[kM], int at) {
+  if constexpr (kStep * 2 < kN) {
+    merge_sorted<kN, kStep * 2>(s, at);
+    merge_sorted<kN, kStep * 2>(s, at + kStep);
+#pragma unroll
+    for (int i = kStep; i + kStep < kN; i += 2 * kStep) exchange(s, at + i, at + i + kStep);
+  } else {
+    exchange(s, at, at + kStep);
+  }
+}
+template <int kN, int kM> __device__ __forceinline__ void sort_down(double (&s)[kM], int at) {
+  if constexpr (kN > 1) {
+    sort_down<kN / 2>(s, at);
+    sort_down<kN / 2>(s, at + kN / 2);
+    merge_sorted<kN, 1>(s, at);
+  }
+}
+
+// Descending order of s[0 .. kN - 1], which fall or rise and then do the other (a bitonic sequence).
+template <int kN, int kStep, int kM> __device__ __forceinline__ void merge_halves(double (&s)[kM]) {
+  if constexpr (kStep >= 1) {
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) exchange(s, i / kStep * 2 * kStep + i % kStep, i / kStep * 2 * kStep + i % kStep + kStep);
+    merge_halves<kN, kStep / 2>(s);
+  }
+}
+
+// The kTop largest of s in descending order, in s[0 .. kTop - 1].
+template <int kTop, int kM> __device__ __forceinline__ void sort_top(double (&s)[kM]) {
+  if constexpr (kTop == kM) {
+    sort_down<kM>(s, 0);
+  } else {
+    static_assert(kM == 2 * kTop, "half or all");
+    sort_down<kTop>(s, 0);
+    sort_down<kTop>(s, kTop);
+#pragma unroll
+    for (int i = 0; i < kTop; ++i) s[i] = larger(s[i], s[kM - 1 - i]);   // the kTop largest: up, then down
+    merge_halves<kTop, kTop / 2>(s);
+  }
+}
+
+// The heads of the list that won move up.
+template <int kTop, int kAt = 0, int kM> __device__ __forceinline__ void move_up(double (&s)[kM], bool won) {
+  if constexpr (kAt + 1 < kTop) {
+    s[kAt] = won ? s[kAt + 1] : s[kAt];
+    move_up<kTop, kAt + 1>(s, won);
+  } else {
+    s[kAt] = won ? 0. : s[kAt];
+  }
+}
+
+// exp(d) for d <= 0 or finite results: 2^t for t = d log2(e) rounded, times what the rounding of t left.
+__device__ __forceinline__ float exp_near(float d) {
+  constexpr float kHi = 1.4426950216293335f, kLo = 1.925963033500011e-8f;   // log2(e) in two parts
+  const float t = d * kHi, e = __builtin_amdgcn_exp2f(t);
+  const float r = __builtin_fmaf(d, kLo, __builtin_fmaf(d, kHi, -t));
+  return __builtin_fmaf(e, r * 0.69314718f, e);
+}
+
+__device__ __forceinline__ float sigmoid(float x) {
+  const float s = __builtin_amdgcn_rcpf(1.f + exp_near(-x));
+  return x > 88.f ? 1.f : x < -88.f ? 0.f : s;   // exp(88) is the last that fits
+}
 
 // exp(x - top): 1 for the largest logits themselves (+infinity too), 0 for -infinity.
-__device__ __forceinline__ float weight(float x, float top) { return x == top ? (top == -INFINITY ? 0.f : 1.f) : expf(x - top); }
+__device__ __forceinline__ float weight(float x, float top) {
+  const float d = x - top;
+  return x == top ? (top == -INFINITY ? 0.f : 1.f) : d < -104.f ? 0.f : exp_near(d);
+}
 
 // NaN counts as -infinity.
 __device__ __forceinline__ float no_nan(float x) { return x == x ? x : -INFINITY; }
@@ -83,8 +160,8 @@ __device__ __forceinline__ float logit(const GateArgs& a, int64_t t, int e) {
   return no_nan(load_elem(a.logits, a.bf16 ? SGT_BF16 : SGT_F32, t * a.stride + e));
 }
 
-// kL lanes per token, kSlots experts per lane, kPicks choices per lane at most.
-template <int kL, int kSlots, int kPicks>
+// kL lanes per token, kSlots experts per lane, of which at most kTop are chosen; kPicks choices per lane at most.
+template <int kL, int kSlots, int kTop, int kPicks>
 __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
   constexpr int kTokens = 64 / kL;   // per wave
   __shared__ float sc[kWaves * kTokens][kL * kSlots + 1];
@@ -93,6 +170,7 @@ __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
   const bool live = t < a.T;
   const int64_t tc = live ? t : a.T - 1;   // lanes past the end repeat the last token and write nothing
 
+  // (what the call asks for is branched on outside the loops over a lane's experts)
   float x[kSlots];
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) x[q] = -INFINITY;
@@ -116,50 +194,74 @@ __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
       if (j * kSlots + q < a.E) x[q] = logit(a, tc, j * kSlots + q);
   }
   float top = -INFINITY, inv = 0.f;
-  const bool scores = a.bias || (a.n_group > 1 && a.group_top > 1);
-  if (!a.sigmoid) {
+  float by[kSlots];   // what a group is weighed by, and with a bias the choice value
+  if (a.sigmoid) {
+    if (a.bias || a.n_group > 1) {
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) by[q] = sigmoid(x[q]);
+    }
+  } else {
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) top = fmaxf(top, x[q]);
     top = over_token<kL>(top, [](float u, float v) { return fmaxf(u, v); });
     float total = 0.f;
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) total += weight(x[q], top);
+    for (int q = 0; q < kSlots; ++q) {
+      by[q] = weight(x[q], top);
+      total += by[q];
+    }
     total = over_token<kL>(total, [](float u, float v) { return u + v; });
     inv = total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f;
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) by[q] *= inv;
   }
-  auto score = [&](float v) { return a.sigmoid ? sigmoid(v) : weight(v, top) * inv; };
+  if (a.bias) {
+    if (a.wide_bias && (j + 1) * kSlots <= a.E) {
+#pragma unroll
+      for (int q = 0; q < kSlots; q += 4) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.bias + j * kSlots + q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) by[q + i] = no_nan(by[q + i] + v[i]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) by[q] = j * kSlots + q < a.E ? no_nan(by[q] + a.bias[j * kSlots + q]) : -INFINITY;
+    }
+  } else if (a.group_top == 1) {
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) by[q] = x[q];
+  }
+  double c[kSlots];   // what is left to choose from
+  if (a.bias) {
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) c[q] = pack(by[q], j * kSlots + q);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) c[q] = pack(x[q], j * kSlots + q);
+  }
+  if ((j + 1) * kSlots > a.E) {
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q)
+      if (j * kSlots + q >= a.E) c[q] = 0.;
+  }
 
   // Groups whose lanes are whole (kSlots divides a group, the group's lanes are 1, 2, 4, 8 or 16) are weighed in registers,
   // others through LDS.
   const int per = a.E / a.n_group, span = per / kSlots;
   const bool grouped = a.n_group > 1, whole = kL == 16 && per % kSlots == 0 && (span & (span - 1)) == 0;
-  double c[kSlots];   // what is left to choose from
   float b1 = -INFINITY, b2 = -INFINITY;
   auto add = [&](float v) {   // the two largest so far
     b2 = fmaxf(b2, fminf(b1, v));
     b1 = fmaxf(b1, v);
   };
-#pragma unroll
-  for (int q = 0; q < kSlots; ++q) {
-    const int e = j * kSlots + q;
-    float v = x[q], by = v;   // the choice value, and what its group is weighed by
-    if (scores) {
-      by = score(v);
-      if (a.bias) v = by = e < a.E ? no_nan(by + a.bias[e]) : -INFINITY;
-    }
-    if (grouped) {
-      if (whole) add(by);
-      else sc[slot][e] = by;
-    }
-    c[q] = e < a.E ? pack(v, e) : 0.;
-  }
-
   if (grouped) {
     constexpr int kR = 64 / kL;
     double g[kR];       // candidates: this lane's groups (several lanes may hold the same one)
     int id[kR];
     auto worth = [&] { return no_nan(a.group_top > 1 ? b1 + b2 : b1); };
     if (whole) {
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) add(by[q]);
       auto merge = [&](float o1, float o2) {
         b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
         b1 = fmaxf(b1, o1);
@@ -175,6 +277,8 @@ __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
       }
       if (id[0] < a.n_group) g[0] = pack(worth(), id[0]);
     } else {
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) sc[slot][j * kSlots + q] = by[q];
       __builtin_amdgcn_wave_barrier();   // a token's lanes are one wave's
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
@@ -198,26 +302,30 @@ __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
 #pragma unroll
       for (int r = 0; r < kR; ++r) g[r] = id[r] == best ? 0. : g[r];
     }
-    int group = j * kSlots / per, in = j * kSlots % per;
+    if (whole) {
+      const bool keep = (kept >> (j / span & 63)) & 1;
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
-      if (!((kept >> (group & 63)) & 1)) c[q] = 0.;
-      if (++in == per) {
-        in = 0;
-        ++group;
+      for (int q = 0; q < kSlots; ++q) c[q] = keep ? c[q] : 0.;
+    } else {
+      int group = j * kSlots / per, in = j * kSlots % per;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        if (!((kept >> (group & 63)) & 1)) c[q] = 0.;
+        if (++in == per) {
+          in = 0;
+          ++group;
+        }
       }
     }
   }
 
   int pick[kPicks] = {};   // lane j keeps choices j, j + kL, ...
+  sort_top<kTop>(c);
   for (int i = 0; i < a.k; ++i) {
-    double m = c[0];
-#pragma unroll
-    for (int q = 1; q < kSlots; ++q) m = larger(m, c[q]);
-    m = over_token<kL>(m, larger);
+    const double m = over_token<kL>(c[0], larger);
     const int e = expert_of(m);
-#pragma unroll
-    for (int q = 0; q < kSlots; ++q) c[q] = j * kSlots + q == e ? 0. : c[q];
+    const bool won = (uint32_t)e / kSlots == (uint32_t)j;
+    move_up<kTop>(c, won);
 #pragma unroll
     for (int r = 0; r < kPicks; ++r) pick[r] = j + kL * r == i ? e : pick[r];
   }
@@ -225,7 +333,9 @@ __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
   float w[kPicks], sum = 0.f;
 #pragma unroll
   for (int r = 0; r < kPicks; ++r) {
-    w[r] = j + kL * r < a.k ? score(logit(a, tc, pick[r])) : 0.f;
+    const float v = logit(a, tc, pick[r]);   // (choice 0 in lanes without one)
+    w[r] = a.sigmoid ? sigmoid(v) : weight(v, top) * inv;
+    if (j + kL * r >= a.k) w[r] = 0.f;
     sum += w[r];
   }
   sum = over_token<kL>(sum, [](float u, float v) { return u + v; });
@@ -239,25 +349,31 @@ __global__ void __launch_bounds__(64 * kWaves) moe_gate_kernel(GateArgs a) {
     }
 }
 
-template <int kL, int kSlots>
+template <int kL, int kSlots, int kTop, int kPicks>
 hipError_t launch(const GateArgs& a, hipStream_t stream) {
   constexpr int kTokens = kWaves * 64 / kL;
   const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(64 * kWaves);
-  if (a.k <= kL)
-    moe_gate_kernel<kL, kSlots, 1><<<grid, block, 0, stream>>>(a);
-  else
-    moe_gate_kernel<kL, kSlots, (64 + kL - 1) / kL><<<grid, block, 0, stream>>>(a);
+  moe_gate_kernel<kL, kSlots, kTop, kPicks><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <int kL, int kSlots>
+hipError_t launch_lanes(const GateArgs& a, hipStream_t stream) {
+  constexpr int kAll = (64 + kL - 1) / kL;   // choices per lane at most
+  if constexpr (kSlots > 8)
+    if (a.k <= 8) return launch<kL, kSlots, 8, 1>(a, stream);
+  if (a.k <= kL) return launch<kL, kSlots, kSlots, 1>(a, stream);
+  return launch<kL, kSlots, kSlots, kAll>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_moe_gate(const GateArgs& a, hipStream_t stream) {
   // 16 lanes take a token of up to 256 experts, so that a round's exchanges serve four tokens; more experts a whole wave
-  if (a.E <= 64) return launch<16, 4>(a, stream);
-  if (a.E <= 128) return launch<16, 8>(a, stream);
-  if (a.E <= 256) return launch<16, 16>(a, stream);
-  return launch<64, 16>(a, stream);
+  if (a.E <= 64) return launch_lanes<16, 4>(a, stream);
+  if (a.E <= 128) return launch_lanes<16, 8>(a, stream);
+  if (a.E <= 256) return launch_lanes<16, 16>(a, stream);
+  return launch_lanes<64, 16>(a, stream);
 }
 
 }  // namespace sgt
