@@ -57,11 +57,17 @@ struct Tile1 {
   int tile;       // row tile inside the sequence
 };
 
-__device__ __forceinline__ int wave_sum_i(int v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+// Sum and maximum over the wave, in a scalar register: DPP exchanges inside each row of 16 lanes, then the four rows.
+template <class F> __device__ __forceinline__ int over_wave(int v, F f) {
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));    // quad swaps
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true));   // half-row and row mirrors
+  v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true));
+  return f(f(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+           f(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
 }
+__device__ __forceinline__ int wave_sum_i(int v) { return over_wave(v, [](int x, int y) { return x + y; }); }
+__device__ __forceinline__ int wave_max_i(int v) { return over_wave(v, [](int x, int y) { return max(x, y); }); }
 
 // Row tiles of sequence s (0 past the end).
 __device__ __forceinline__ int seq_tiles(const PromptArgs& a, int s, int G, int rows) {
@@ -81,9 +87,7 @@ __device__ __forceinline__ Tile1 find_tile(const PromptArgs& a, int w, int G, in
   const int mine = seq_tiles(a, lane, G, rows);
   int top = mine;
   for (int c = 64; c < a.n_seqs; c += 64) top = max(top, seq_tiles(a, c + lane, G, rows));
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
-  top = uniform(top);
+  top = wave_max_i(top);
   auto above = [&](int level) {   // tiles at levels >= level
     int n = max(mine - level, 0);
     if (!one)
@@ -92,13 +96,13 @@ __device__ __forceinline__ Tile1 find_tile(const PromptArgs& a, int w, int G, in
   };
   Tile1 t{};
   t.seq = -1;
-  if (uniform(above(0)) <= w) return t;
+  if (above(0) <= w) return t;
   int lo = 0, hi = top;           // above(lo) > w, above(hi) = 0
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (uniform(above(mid)) > w) lo = mid; else hi = mid;
+    if (above(mid) > w) lo = mid; else hi = mid;
   }
-  int k = w - uniform(above(lo + 1));      // place inside level lo
+  int k = w - above(lo + 1);      // place inside level lo
   int s = 0;
   for (int c = 0; c < a.n_seqs; c += 64) {
     uint64_t has = __ballot((c == 0 ? mine : seq_tiles(a, c + lane, G, rows)) > lo);
