@@ -36,22 +36,10 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
-}
-
 // Maximum of non-negative floats by their bits: a NaN is the largest of all, so it is not lost as fmaxf would lose it.
 __device__ __forceinline__ float abs_max(float top, float v) {
   const uint32_t a = __float_as_uint(top), b = __float_as_uint(v) & 0x7FFFFFFFu;
   return __uint_as_float(a > b ? a : b);
-}
-
-__device__ __forceinline__ float wave_abs_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = abs_max(v, __shfl_xor(v, o));
-  return v;
 }
 
 constexpr float kF8Max = 448.f;             // largest e4m3 value

@@ -1,17 +1,20 @@
 // Root-mean-square norm with the residual's addition, and an output in bf16,
 // fp32 or 8 bits with scales.
 //
-// The bytes bound this: x and the residual are read once, the sum and the output
-// written once.  A row stays in registers between the sum of its squares and its
-// scaling: thread t of a row's `lanes` threads holds the vectors of 8 elements t,
-// t + lanes, ... (kN of them), each read and written with one 16-byte access per
-// 16 bytes.  Rows may start at any element: the accesses need no alignment, and
-// the last H % 8 elements of a row are taken one by one by the thread whose
+// y = s w / sqrt(mean s^2 + eps) of s = x + residual; the sum of squares and the scaling in fp32.  s is rounded once, to
+// the residual's type, where it is stored (y is made from the unrounded s), and y once, to the output's type.  8 bits: the
+// scale of a row or of 128 columns is its largest |y| / 448, and y / scale is rounded to e4m3.
+//
+// The bytes bound this: x and the residual are read once, the sum and the output written once.  A row stays in registers
+// between the sum of its squares and its scaling: thread t of a row's `lanes` threads holds the vectors of 8 elements t,
+// t + lanes, ... (kN of them), each read and written with one 16-byte access per 16 bytes.  Rows may start at any
+// element: the accesses need no alignment, and the last H % 8 elements of a row are taken one by one by the thread whose
 // vector they would begin.
 //
-// A row of up to 512 kN elements is one wave's (four rows per workgroup, no
-// barrier); a longer one takes a workgroup, whose waves exchange their sums
-// through LDS.
+// Measured: 2048 x 8192 fp32 rows with a bf16 residual and output 29.7 us (168 MB at 5.6 TB/s; a 2 GiB copy reaches 4.9
+// here), 8191 x 5120 bf16 to 8 bits 60.9 us (295 MB at 4.8 TB/s).  One row of 8192 takes 3.6 us, three times the
+// memory's latency and the launch.  Stores past the L2 were worth 37.5 -> 34.7 and 69.4 -> 64.6 us, one or two vectors per
+// thread instead of four the rest.
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
@@ -22,6 +25,7 @@ namespace sgt {
 namespace {
 
 constexpr int kVec = 8;
+constexpr int kThreads = 256;   // of a workgroup that holds several rows
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -34,7 +38,11 @@ template <class T> __device__ __forceinline__ T load_any(const void* p) {
   return v;
 }
 
-template <class T> __device__ __forceinline__ void store_any(void* p, T v) { __builtin_memcpy(p, &v, sizeof v); }
+// Past the L2 (nontemporal): nothing here reads it again, and it would push out the rows that are still to be read.
+template <class T> __device__ __forceinline__ void store_any(void* p, T v) {
+  typedef T any_t __attribute__((aligned(1)));
+  __builtin_nontemporal_store(v, static_cast<any_t*>(p));
+}
 
 // n (1 .. 8) elements from element `at` on; the missing ones are zero.
 template <bool kF32>
@@ -104,21 +112,27 @@ __device__ __forceinline__ void write_vec(void* p, int dtype, int64_t at, int n,
     }
 }
 
-// Largest magnitude over 16 neighbouring lanes.
-__device__ __forceinline__ float row16_abs_max(float v) {
+// Sum and largest magnitude over kLanes neighbouring lanes.
+template <int kLanes> __device__ __forceinline__ float sum_over(float v) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = abs_max(v, __shfl_xor(v, o));
+  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+template <int kLanes> __device__ __forceinline__ float abs_max_over(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v = abs_max(v, __shfl_xor(v, o));
   return v;
 }
 
-// kWave: a row is one wave's; else the workgroup's.
-template <bool kF32, int kN, bool kWave>
-__global__ void __launch_bounds__(kWave ? 256 : 1024) rms_norm_kernel(NormArgs a) {
+// A row is kLanes neighbouring lanes', or with kLanes = 0 the workgroup's.
+template <bool kF32, int kN, int kLanes>
+__global__ void __launch_bounds__(kLanes ? kThreads : 1024) rms_norm_kernel(NormArgs a) {
   __shared__ float red[2][16];
+  constexpr int kIn = kLanes ? kLanes : 64;   // a row's lanes inside a wave
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int lanes = kWave ? 64 : (int)blockDim.x, t = kWave ? lane : (int)threadIdx.x;
-  const int64_t row = kWave ? (int64_t)blockIdx.x * 4 + wv : (int64_t)blockIdx.x;
-  if (kWave && row >= a.T) return;
+  const int lanes = kLanes ? kLanes : (int)blockDim.x, t = kLanes ? lane % kIn : (int)threadIdx.x;
+  const int64_t row = kLanes ? (int64_t)blockIdx.x * (kThreads / kIn) + threadIdx.x / kIn : (int64_t)blockIdx.x;
+  if (kLanes && row >= a.T) return;   // all of a row's lanes; nothing below reaches past them
   const int64_t x0 = row * a.x_stride, r0 = row * a.H;
   float s[kN][kVec];
   float ss = 0.f;
@@ -140,8 +154,8 @@ __global__ void __launch_bounds__(kWave ? 256 : 1024) rms_norm_kernel(NormArgs a
 #pragma unroll
     for (int j = 0; j < kVec; ++j) ss += s[i][j] * s[i][j];
   }
-  ss = wave_sum(ss);
-  if constexpr (!kWave) {
+  ss = sum_over<kIn>(ss);
+  if constexpr (kLanes == 0) {
     if (lane == 0) red[0][wv] = ss;
     __syncthreads();
     ss = 0.f;
@@ -165,8 +179,8 @@ __global__ void __launch_bounds__(kWave ? 256 : 1024) rms_norm_kernel(NormArgs a
   }
   if (a.out_dtype != SGT_F8E4M3) return;
   if (a.block == 0) {
-    top = wave_abs_max(top);
-    if constexpr (!kWave) {
+    top = abs_max_over<kIn>(top);
+    if constexpr (kLanes == 0) {
       if (lane == 0) red[1][wv] = top;
       __syncthreads();
       for (int i = 0; i < lanes / 64; ++i) top = abs_max(top, red[1][i]);
@@ -180,40 +194,50 @@ __global__ void __launch_bounds__(kWave ? 256 : 1024) rms_norm_kernel(NormArgs a
       top = 0.f;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) top = abs_max(top, j < n ? s[i][j] : 0.f);
-      top = row16_abs_max(top);
+      top = abs_max_over<16>(top);
       if (n > 0 && (lane & 15) == 0) a.scales[row * ((a.H + 127) / 128) + at / 128] = f8_scale(top);
     }
     if (n <= 0) continue;
-    const float scale = f8_scale(top);
+    const float scale = f8_scale(top), r = 1.f / scale, back = scale < INFINITY ? scale : 0.f;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) s[i][j] = s[i][j] / scale;
+    for (int j = 0; j < kVec; ++j) {   // s / scale, the product's error taken back (an infinite scale leaves 0)
+      const float q = s[i][j] * r;
+      s[i][j] = __builtin_fmaf(__builtin_fmaf(-q, back, s[i][j]), r, q);
+    }
     write_vec(a.out, SGT_F8E4M3, r0 + at, n, s[i]);
   }
 }
 
+template <bool kF32, int kLanes>
+hipError_t launch_lanes(const NormArgs& a, hipStream_t stream) {
+  constexpr int kRows = kThreads / kLanes;
+  rms_norm_kernel<kF32, 1, kLanes><<<dim3((unsigned)((a.T + kRows - 1) / kRows)), dim3(kThreads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <bool kF32, int kN>
 hipError_t launch(const NormArgs& a, int vecs, hipStream_t stream) {
-  if (vecs <= 64 * kN) {
-    rms_norm_kernel<kF32, kN, true><<<dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, stream>>>(a);
-  } else {
-    const int lanes = ((vecs + kN - 1) / kN + 63) / 64 * 64;
-    rms_norm_kernel<kF32, kN, false><<<dim3((unsigned)a.T), dim3((unsigned)lanes), 0, stream>>>(a);
-  }
+  const int lanes = ((vecs + kN - 1) / kN + 63) / 64 * 64;
+  rms_norm_kernel<kF32, kN, 0><<<dim3((unsigned)a.T), dim3((unsigned)lanes), 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <bool kF32>
 hipError_t launch_type(const NormArgs& a, hipStream_t stream) {
+  // Rows of up to 128 elements: 16 lanes each, or most of a wave would idle (65536 x 128: 12.0 us, by whole waves 21.6).
+  // Up to 512: a wave each, without barriers (1 x 512: 2.9 us, and 2.9 by a workgroup; 65536 x 128 bf16 21.8 and 22.4).
+  // Longer rows take a workgroup and as few vectors per thread as fit, the rest of the latency hidden by other rows:
+  // 1 x 8192 at 1 / 2 / 4 vectors 3.6 / 4.1 / 5.8 us, 8191 x 2048 21.6 / 22.3 / 26.2.  Past 4096 elements one vector
+  // each makes workgroups of 9 to 16 waves, of which few fit a CU's 32; with rows to spare two are better: 8191 x 5120
+  // bf16 65.6 / 61.4, to 8 bits 67.1 / 61.7, 1024 x 5120 9.5 / 8.3; at 8192 even (bf16 90.6 / 92.8, 8 bits 90.9 / 85.0);
+  // 256 rows of 5120 4.4 / 5.0.
   const int vecs = (a.H + kVec - 1) / kVec;
-  // Many rows fill the chip by themselves: four vectors in flight per thread.  Few rows: one each, so that the row's
-  // loads are spread over as many waves as it has.  Rows past 8 x 1024 x 4 elements take eight.
-  const int n = vecs > 4096 ? 8 : a.T >= 256 || vecs > 1024 ? (vecs > 128 ? 4 : 2) : 1;
-  switch (n) {
-    case 1: return launch<kF32, 1>(a, vecs, stream);
-    case 2: return launch<kF32, 2>(a, vecs, stream);
-    case 4: return launch<kF32, 4>(a, vecs, stream);
-    default: return launch<kF32, 8>(a, vecs, stream);
-  }
+  if (vecs <= 16) return launch_lanes<kF32, 16>(a, stream);
+  if (vecs <= 64) return launch_lanes<kF32, 64>(a, stream);
+  if (vecs > 4096) return launch<kF32, 8>(a, vecs, stream);
+  if (vecs > 2048) return launch<kF32, 4>(a, vecs, stream);
+  if (vecs > 1024 || (vecs > 512 && a.T >= 512)) return launch<kF32, 2>(a, vecs, stream);
+  return launch<kF32, 1>(a, vecs, stream);
 }
 
 }  // namespace

@@ -135,6 +135,38 @@ def test_norm_zero_rows_nan_rows_and_extremes():
         assert (out[3].float() == 448).all()
 
 
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("H", [128, 640, 8192])
+def test_norm_8bit_infinite_scale(H, block):
+    """An infinite weight makes the scale infinite: what is finite beside it becomes 0, infinity over infinity NaN."""
+    x, w = torch.ones(600, H, device=DEV), torch.ones(H, device=DEV)
+    w[70] = INF
+    out = torch.empty(600, H, dtype=torch.float8_e4m3fn, device=DEV)
+    scales = torch.empty(600, (H + 127) // 128 if block else 1, device=DEV)
+    sgt.rms_norm(x, w, out, scales=scales)
+    assert torch.isinf(scales[:, 0]).all() and torch.isfinite(scales[:, 1:]).all()
+    got = out.float()
+    assert torch.isnan(got[:, 70]).all() and (got[:, :70] == 0).all() and (got[:, 71:128] == 0).all()
+    assert (got[:, 128:] == (448 if block else 0)).all()
+
+
+@pytest.mark.parametrize("H", [1, 16, 40, 127, 128, 136, 512])
+@pytest.mark.parametrize("T", [15, 16, 1041])
+def test_norm_short_rows(T, H):
+    rng = np.random.default_rng(T + H)
+    x, w = rnd(rng, (T, H), torch.float32), rnd(rng, (H,), torch.float32)
+    _, y_ref = L.rms_norm(f64(x), None, f64(w), 1e-6)
+    y = torch.full((T + 1, H), 7.0, device=DEV)
+    sgt.rms_norm(x, w, y[:T])
+    near(y[:T], y_ref, 4e-6, 1e-9)
+    assert (y[T] == 7).all()
+    out, scales = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=DEV), torch.empty(T, 1, device=DEV)
+    sgt.rms_norm(x, w, out, scales=scales)
+    scales_ref = L.f8_scales(y_ref, 0)
+    near(scales, scales_ref, 4e-6)
+    near(out, y_ref / scales_ref, 2.0 ** -4 + 1e-5, 2.0 ** -10 + 1e-5)
+
+
 def test_norm_many_rows_past_32_bits():
     H, T = 8192, 262144 + 3   # 2^31 elements and more
     x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
