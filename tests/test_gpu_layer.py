@@ -233,6 +233,16 @@ def test_gate_groups_and_bias(E, g, kept, k, score, top):
     check_gate(x, k, score=score, n_group=g, topk_group=kept, group_top=1, renormalize=False)
 
 
+@pytest.mark.parametrize("E,g,kept,k", [(512, 8, 4, 8), (384, 8, 3, 6), (320, 2, 1, 3), (512, 2, 1, 20), (1024, 64, 5, 8), (1024, 4, 2, 64)])
+@pytest.mark.parametrize("top", [1, 2])
+def test_gate_groups_of_many_experts(E, g, kept, k, top):
+    rng = np.random.default_rng(E + g + k)
+    x = grid(rng, (67, E), 2.0 ** -6, -300, 300)
+    bias = torch.from_numpy(rng.standard_normal(E).astype(np.float32)).to(DEV)
+    check_gate(clearly_apart(x, bias, "sigmoid", g, top), k, score="sigmoid", bias=bias, n_group=g, topk_group=kept, group_top=top)
+    check_gate(x[:3], k, score="softmax", n_group=g, topk_group=kept, group_top=1)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_gate_types_strides_and_ties(dtype):
     rng = np.random.default_rng(3)
