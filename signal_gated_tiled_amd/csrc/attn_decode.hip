@@ -4,14 +4,12 @@
 // 16 kNQ query heads that share it, on the matrix cores (the heads as columns), so
 // that the arithmetic stays far below the memory's time.
 //
-// Split and join.  The work is a list of problems (sequence, key head, chunk of
-// query heads), each a row of tiles of 2 KiB / D keys; the tiles of all problems,
-// one after another, are cut into equal ranges, one per workgroup, whatever the
-// lengths (a problem counts kProblemCost tiles more than it has, for the latency of
-// its start and its join).  A workgroup that holds all of a problem's tiles writes the result; else
-// it writes its part (unnormalised output, maximum, sum) to the workspace and counts
-// itself in, and the last one to do so joins the parts in their order, so the
-// bits do not depend on who came last.
+// Split and join.  The work is a list of problems (sequence, key head, chunk of query heads), each a row of tiles of 2 KiB
+// / D keys; the tiles of all problems, one after another, are cut into equal ranges, one per workgroup, whatever the
+// lengths (a problem counts kProblemCost tiles more than it has, for the latency of its start and its join).  A workgroup
+// that holds all of a problem's tiles writes the result; else it writes its part (unnormalised output, maximum, sum) to
+// the workspace and counts itself in, and the last of up to kFan neighbours joins their parts in order, all loads at
+// once; of several such joins the last one joins those.  So the bits do not depend on who came last.
 //
 // Inside a workgroup the four waves take every fourth tile each, without
 // barriers: each wave has a ring of four LDS stages of its own, filled by
@@ -26,6 +24,8 @@
 // pass 2^8.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attn.hpp"
 #include "layer.hpp"
 #include "signal.hpp"
@@ -37,11 +37,19 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRing = 4;                      // LDS stages of a wave
 constexpr int kGrid = 256;                   // workgroups: one on each CU (128 KiB of LDS)
-constexpr int kMinTiles = 4;                 // tiles of a range at least: one for each wave
-constexpr int kMaxParts = 64;                // a problem is cut into about this many parts at most
-constexpr int kProblemCost = 24;             // what starting and joining a problem costs a workgroup, in tiles
+// Tiles of a range at least: one for each wave.  (us at 4 / 8 / 16 tiles, one sequence, 8 query heads and 1 key head:
+// 100 keys 9.1 / 8.1 / 8.1, 777 keys 10.5 / 11.2 / 11.7, 4096 keys 13.5 / 14.1 / 13.0, 16384 keys 15.4 / 14.8 / 15.7)
+constexpr int kMinTiles = 4;
+// What starting and joining a problem costs a workgroup, in tiles.  (us at 0 / 8 / 24 / 48: 128 sequences of 1 to 16000
+// keys 63 / 39 / 34 / 35, 64 of 1000 with 4 key heads 49 / 40 / 37 / 37, 256 of 1 to 300 20.5 / 13.9 / 13.3 / 13.4)
+constexpr int kProblemCost = 24;
+// Parts joined at once; a problem has at most kFan^2, one in each workgroup.  (One sequence of 131072 keys and 1 key head:
+// 26.4 us in 256 parts and two levels; 43 when cut into 64 parts joined by one workgroup in four rounds.)
+constexpr int kFan = 16;
 constexpr int kMaxRows = 32;                 // query heads of a chunk
-constexpr int kSlotFloats = kMaxRows * 128 + 2 * kMaxRows;   // one part: outputs, maxima, sums
+constexpr int kSlotStats = kMaxRows * 128;    // one part: outputs, maxima and sums, then the maxima and sums of kFan joined
+constexpr int kSlotFloats = kSlotStats + 4 * kMaxRows;
+static_assert(kGrid <= kFan * kFan, "two levels join every part");
 
 typedef const __attribute__((address_space(1))) uint8_t* gptr_t;
 typedef const __attribute__((address_space(1))) void* gvoid_t;
@@ -119,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
 
   // this workgroup's range of the units (of each problem its tiles, then its cost)
   int64_t total = 0, end0 = 0, total0 = 0;   // end0, total0: of the first kThreads sequences
-  int top = 0, cost0 = 0;
+  int cost0 = 0;
   for (int c = 0; c < a.B; c += kThreads) {
     const int n = tiles_of<kT>(a, c + tid, room), cost = n > 0 ? n + kProblemCost : 0;
     int64_t t;
@@ -130,19 +138,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       cost0 = cost;
     }
     total += t;
-    top = max(top, n);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
-  __syncthreads();
-  if (lane == 0) red[w] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) top = max(top, (int)red[i]);
-  top = uniform(top);
   const int64_t units = uniform(total) * HC;
   const int64_t grid = gridDim.x;
-  const int64_t chunk = max(max(quotient(units + grid - 1, grid), (int64_t)kMinTiles), (int64_t)((top + kMaxParts - 1) / kMaxParts));
+  const int64_t chunk = max(quotient(units + grid - 1, grid), (int64_t)kMinTiles);
   const int64_t u0 = blockIdx.x * chunk, u1 = min(u0 + chunk, units);
   if (u0 >= units) return;
   for (int64_t c = 0, before = 0; c < a.B; c += kThreads) {
@@ -344,6 +343,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       wait_vm<0>();   // the repeated loads too, before the stages are used for the join
     }
 
+    // columns 4 at .. 4 at + 3 of row r, from their sum, the row's maximum and the sum of its weights
+    auto finish = [&](int r, int at, f32x4_t v, float M, float L) {
+      const float inv = 1.f / L;
+      v = L == 0.f ? f32x4_t{0.f, 0.f, 0.f, 0.f} : v * inv;
+      const int64_t to = ((int64_t)b * a.Hq + h0 + r) * kD + 4 * at;
+      if (a.out_f32)
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + to) = v;
+      else
+        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      if (a.lse && at == 0) a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    };
+
     // join the waves: each scales its output to the common maximum and leaves it in its stage
     const int jl = fresh_lane(), jt = w * 64 + jl, jg = jl >> 4, jc = jl & 15;
     const bool whole = ta == 0 && tb == n_tiles;
@@ -386,91 +397,85 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
           L += mx == -INFINITY ? lx : lx * __builtin_amdgcn_exp2f(mx - Mr);
         }
         if (whole) {
-          const float inv = 1.f / L;
-          v = L == 0.f ? f32x4_t{0.f, 0.f, 0.f, 0.f} : v * inv;
-          const int64_t to = ((int64_t)b * a.Hq + h0 + r) * kD + 4 * at;
-          if (a.out_f32)
-            *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + to) = v;
-          else
-            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-          if (a.lse && at == 0)
-            a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (Mr + __builtin_amdgcn_logf(L)) * kLn2;
+          finish(r, at, v, Mr, L);
         } else {
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rp, (uint32_t)(r * kD + 4 * at) * 4, 0, kCpolSc1);
-          if (at == 0) {
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(Mr), rp, (uint32_t)(kMaxRows * 128 + r) * 4, 0, kCpolSc1);
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(L), rp, (uint32_t)(kMaxRows * 129 + r) * 4, 0, kCpolSc1);
-          }
+          if (at == 0)
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(Mr), __float_as_uint(L)}, rp, (uint32_t)(kSlotStats + 2 * r) * 4, 0, kCpolSc1);
         }
       }
       __syncthreads();
     }
 
     if (!whole) {
-      // the parts went to the device's coherence point; once every wave's stores are acknowledged this workgroup counts
-      // itself in, and the last one of the problem joins all parts in order
-      const int64_t w_last = quotient(start + n_tiles - 1, chunk);
-      const int n_parts = (int)(w_last - w_first) + 1;
-      uint32_t* counter = counters + (int64_t)b * HC + hc;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (jt == 0) {
-        const uint32_t seen = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        last = seen == (uint32_t)n_parts - 1;
-        if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // ready for the next call
-      }
-      __syncthreads();
-      if (last) {
+      // The parts went to the device's coherence point.  Once every wave's stores are acknowledged this workgroup counts
+      // itself in among its kFan parts, and the last of them joins them in order; of several such joins the last one
+      // joins those.
+      const int n_parts = (int)(quotient(start + n_tiles - 1, chunk) - w_first) + 1, mine = (int)(blockIdx.x - w_first);
+      auto slot_of = [&](int p) { return (int)(w_first + p) * 2 + (p == 0 && inside ? 1 : 0); };   // later parts: the first slot
+      auto is_last = [&](uint32_t* counter, int n) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (jt == 0) {
+          const uint32_t seen = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          last = seen == (uint32_t)n - 1;
+          if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // ready for the next call
+        }
+        __syncthreads();
+        return last != 0;
+      };
+      const __amdgpu_buffer_rsrc_t ra = make_rsrc(parts, (uint64_t)kGrid * 2 * kSlotFloats * 4);
+      // Join n parts first, first + by, ..., whose maxima and sums lie at `stats`: into the first one's slot, or the result.
+      // kAtOnce >= n of them are loaded together.
+      auto join = [&](auto at_once, int first, int by, int n, int stats, bool result) {
+        constexpr int kAtOnce = decltype(at_once)::value;
         acquire_agent();
-        const int64_t s_first = w_first * 2 + (inside ? 1 : 0);   // later parts lie in their workgroup's first slot
-        const __amdgpu_buffer_rsrc_t ra = make_rsrc(parts, (uint64_t)kGrid * 2 * kSlotFloats * 4);
         for (int e = jt; e < nh * kD / 4; e += kThreads) {
           const int r = e / (kD / 4), at = e % (kD / 4);
-          auto off = [&](int i, int f) {
-            return (uint32_t)(((i == 0 ? s_first : (w_first + i) * 2) * kSlotFloats + f) * 4);
+          auto off = [&](int i, int f) {   // past the last part: out of the buffer's range, which reads as 0
+            return i < n ? (uint32_t)(slot_of(first + i * by) * kSlotFloats + f) * 4 : 0xFFFFFF00u;
           };
+          float mi[kAtOnce], li[kAtOnce];
+          f32x4_t xi[kAtOnce];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const u32x2_t ml = __builtin_amdgcn_raw_buffer_load_b64(ra, off(i, stats + 2 * r), 0, kCpolSc1);
+            mi[i] = __uint_as_float(ml[0]);
+            li[i] = __uint_as_float(ml[1]);
+            xi[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, off(i, r * kD + 4 * at), 0, kCpolSc1));
+          }
           float M = -INFINITY, L = 0.f;
           f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-          constexpr int kAtOnce = 16;   // parts whose loads are in flight together
-          for (int i0 = 0; i0 < n_parts; i0 += kAtOnce) {
-            float mi[kAtOnce], li[kAtOnce];
-            f32x4_t xi[kAtOnce];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-              const int i = min(i0 + u, n_parts - 1);
-              mi[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, off(i, kMaxRows * 128 + r), 0, kCpolSc1));
-              li[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, off(i, kMaxRows * 129 + r), 0, kCpolSc1));
-              xi[u] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, off(i, r * kD + 4 * at), 0, kCpolSc1));
-            }
-            float Mn = M;
+          for (int i = 0; i < kAtOnce; ++i) M = i < n ? fmaxf(M, mi[i]) : M;
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) Mn = fmaxf(Mn, mi[u]);
-            const float f0 = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(M - Mn);
-            M = Mn;
-            L *= f0;
-            v *= f0;
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-              const float f = mi[u] == -INFINITY ? (li[u] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mi[u] - M);
-              if (i0 + u < n_parts) {
-                L += li[u] * f;
-                v += xi[u] * f;
-              }
+          for (int i = 0; i < kAtOnce; ++i) {
+            const float f = mi[i] == -INFINITY ? (li[i] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mi[i] - M);
+            if (i < n) {
+              L += li[i] * f;
+              v += xi[i] * f;
             }
           }
-          const float inv = 1.f / L;
-          v = L == 0.f ? f32x4_t{0.f, 0.f, 0.f, 0.f} : v * inv;
-          const int64_t to = ((int64_t)b * a.Hq + h0 + r) * kD + 4 * at;
-          if (a.out_f32)
-            *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + to) = v;
-          else
-            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + to) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-          if (a.lse && at == 0)
-            a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+          if (result) {
+            finish(r, at, v, M, L);
+          } else {
+            const int to = slot_of(first) * kSlotFloats;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), ra, (uint32_t)(to + r * kD + 4 * at) * 4, 0, kCpolSc1);
+            if (at == 0)
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(M), __float_as_uint(L)}, ra,
+                                                    (uint32_t)(to + kSlotStats + 2 * (kMaxRows + r)) * 4, 0, kCpolSc1);
+          }
         }
+      };
+      const int first = mine / kFan * kFan, n = min(kFan, n_parts - first);
+      if (is_last(counters + slot_of(first), n)) {
+        if (n_parts <= 4) join(std::integral_constant<int, 4>(), first, 1, n, kSlotStats, true);
+        else join(std::integral_constant<int, kFan>(), first, 1, n, kSlotStats, n_parts <= kFan);
+        const int groups = (n_parts + kFan - 1) / kFan;
+        if (groups > 1 && is_last(counters + 2 * kGrid + slot_of(0), groups))
+          join(std::integral_constant<int, kFan>(), 0, kFan, groups, kSlotStats + 2 * kMaxRows, true);
       }
     }
-
   };
 
   while (true) {
@@ -504,10 +509,9 @@ hipError_t launch(const DecodeArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// The parts' slots have one size whatever the call, so the counters behind them stay zero between calls of any shape.
-int64_t attn_decode_workspace(int B, int Hq, int Hkv, int) {
-  return kPartBytes + ((int64_t)B * Hkv * chunks_of(Hq, Hkv) * 4 + 15) / 16 * 16;
-}
+// Two slots for each workgroup, and for each slot the two counters of the joins that begin with it; the same whatever the
+// call, so that the counters stay zero between calls of any shape.
+int64_t attn_decode_workspace() { return kPartBytes + 4 * kGrid * (int64_t)sizeof(uint32_t); }
 
 hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t stream) {
   if (a.Hq / a.Hkv <= 16) return a.D == 64 ? launch<64, 1>(a, stream) : launch<128, 1>(a, stream);

@@ -67,6 +67,6 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_moe_gate(const GateArgs& a, hipStream_t stream);
 hipError_t launch_attn_prompt(const PromptArgs& a, hipStream_t stream);
 hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t stream);
-int64_t attn_decode_workspace(int B, int Hq, int Hkv, int D);
+int64_t attn_decode_workspace();
 
 }  // namespace sgt

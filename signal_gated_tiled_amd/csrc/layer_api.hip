@@ -137,7 +137,7 @@ int64_t sgt_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
   if (B < 0 || (int64_t)B * Hkv > (1 << 24)) return fail(SGT_EINVAL, "B = %d", B);
   sgt_status st = check_heads(Hq, Hkv, D);
   if (st != SGT_OK) return st;
-  return attn_decode_workspace(B, Hq, Hkv, D);
+  return attn_decode_workspace();
 }
 
 sgt_status sgt_attn_decode(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache, int64_t page_stride,

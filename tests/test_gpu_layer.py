@@ -504,6 +504,23 @@ def test_decode_long_cache():
     check_decode(rng, rnd(rng, (3, 4, 64), std=2.0), k, v, table, n)
 
 
+def test_decode_parts_in_one_workspace():
+    """Caches cut into one to 256 parts, in calls of other shapes after each other on one workspace."""
+    rng = np.random.default_rng(14)
+    ws = workspace(8, 32, 32, 128)
+    for lens, hq, hkv, d in [([1024], 8, 1, 128), ([1030], 8, 1, 128), ([70000], 4, 1, 64), ([1088, 3], 32, 2, 128), ([2100], 8, 1, 128),
+                             ([300] * 8, 32, 32, 64), ([16300], 2, 1, 128), ([40000], 32, 1, 64), ([16400], 3, 1, 128), ([260], 20, 1, 128)]:
+        k, v, table, n = make_cache(rng, lens, 16, hkv, d, fill=NAN)
+        q = rnd(rng, (len(lens), hq, d))
+        ref = L.paged_attention(f64(q), f64(k), f64(v), table.cpu().numpy(), n.cpu().numpy(), d ** -0.5)
+        out, lse = torch.full((len(lens), hq, d), NAN, device=DEV), torch.full((len(lens), hq), NAN, device=DEV)
+        sgt.attn_decode(q, k, v, table, n, out, ws, lse=lse)
+        check_attention(out, lse, ref, True)
+        again, lse2 = torch.empty_like(out), torch.empty_like(lse)
+        sgt.attn_decode(q, k, v, table, n, again, ws, lse=lse2)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_decode_lengths_and_pages_outside():
     rng = np.random.default_rng(12)
     k, v, table, n = make_cache(rng, [100, 100, 100, 100], 16, 1, 128, width=7)
