@@ -37,7 +37,8 @@ def moe_gate(logits, topk: int, score: str = "softmax", bias=None, n_group: int 
                 s = 1.0 / (1.0 + np.exp(-x))
         else:
             m = x.max()
-            s = np.zeros(E) if m == -np.inf else np.where(x == m, 1.0, np.exp(np.where(x == m, 0.0, x - m)))
+            with np.errstate(invalid="ignore"):   # infinity less itself, not taken
+                s = np.zeros(E) if m == -np.inf else np.where(x == m, 1.0, np.exp(np.where(x == m, 0.0, x - m)))
             s = s / s.sum() if s.sum() > 0 else s
         c = x if bias is None else s + np.asarray(bias, np.float64)
         c = np.where(np.isnan(c), -np.inf, c)
