@@ -29,8 +29,8 @@ FLAGS = [
     "-I" + os.path.join(ROOT, "include"), "-I" + CSRC,
 ]
 
-# Flags of one file.  The decode kernel's LDS leaves one wave per SIMD, from which the compiler would conclude that the
-# matrix products had better accumulate in the second half of the register file, and copy its values to and fro.
+# Flags of one file.  The attention kernels' LDS leaves one or two waves per SIMD, from which the compiler would conclude
+# that the matrix products had better accumulate in the second half of the register file, and copy their values to and fro.
 FILE_FLAGS = {"attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"], "attn_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 

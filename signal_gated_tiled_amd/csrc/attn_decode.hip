@@ -22,6 +22,12 @@
 // head per lane column, its registers are the B operand of O^T += V^T P^T, V^T comes
 // from the transposing LDS read, and the maximum moves only when a weight would
 // pass 2^8.
+//
+// Rounding.  Scores, maxima, sums, parts and joins are fp32; the weights are two bf16 parts (16 bits of each weight).
+//
+// Measured: 4 sequences of 90000 to 131072 tokens, 64 query heads on 8, D 128, 305 us (1.75 GB at 5.7 TB/s; a 2 GiB copy
+// reaches 4.9 here); 128 sequences of 1 to 16000, 8 heads on one, 33 us (117 MB at 3.5 TB/s, of which about 8 us are the chain of
+// launch, lengths, page ids, first tile and joins); one of 777 10.2 us, that chain alone.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
