@@ -312,58 +312,66 @@ def gemm_rs_static_scratch_bytes() -> int:
     return int(lib().sgt_gemm_rs_static_scratch_bytes())
 
 
-_torch_module = None
 
 
-def _torch():
-    """The torch module, imported on the first call (an import statement in each call would cost more than its checks)."""
-    global _torch_module
-    if _torch_module is None:
+class _Torch:
+    """The torch module and what the layer operators' calls need of it, looked up on the first call (an import statement or
+    a chain of attributes in each call would cost more than its checks)."""
+
+    def __init__(self):
         import torch
-        _torch_module = torch
-    return _torch_module
+        self.bf16, self.f32, self.f8, self.i32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+        self.codes = {torch.bfloat16: SGT_BF16, torch.float32: SGT_F32}
+        self.device = torch._C._cuda_getDevice
+        self.stream = torch._C._cuda_getCurrentRawStream
 
 
-def _code(dtype) -> int:
+_torch_names = None
+
+
+def _torch() -> _Torch:
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
+def _code(th: _Torch, dtype) -> int:
     """SGT_BF16 or SGT_F32 of a torch dtype."""
-    torch = _torch()
-    if dtype is torch.bfloat16:
-        return SGT_BF16
-    if dtype is torch.float32:
-        return SGT_F32
-    raise TypeError("tensors must be bfloat16 or float32, got %s" % dtype)
+    code = th.codes.get(dtype)
+    if code is None:
+        raise TypeError("tensors must be bfloat16 or float32, got %s" % dtype)
+    return code
 
 
 def _layer_ptr(t, name: str, dtype, shape, device: int) -> int:
     """Device pointer of a dense tensor of this dtype and shape on GPU `device`; None is NULL."""
     if t is None:
         return 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.get_device() != device:
         raise ValueError("%s is on %s, expected GPU %d" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
-def _current_device(t, name: str) -> int:
+def _current_device(th: _Torch, t, name: str) -> int:
     """The GPU of `t`, which must be the calling thread's current one (the layer operators run there)."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("%s must be a GPU tensor" % name)
-    torch = _torch()
-    if torch._C._cuda_getDevice() != dev:
-        raise ValueError("the call runs on the current device (%d); %s is on %s" %
-                         (torch.cuda.current_device(), name, t.device))
+    if th.device() != dev:
+        raise ValueError("the call runs on the current device (%d); %s is on %s" % (th.device(), name, t.device))
     return dev
 
 
-def _layer_stream(stream, device: int) -> int:
+def _layer_stream(th: _Torch, stream, device: int) -> int:
     """Raw handle of `stream`, or of the device's current stream (without building a stream object for it)."""
-    return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return th.stream(device) if stream is None else stream.cuda_stream
 
 
 def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: float = 1e-6, stream=None):
@@ -371,28 +379,29 @@ def rms_norm(x, weight, out, *, residual=None, sum_out=None, scales=None, eps: f
     eps) * weight.  x: T x H fp32 or bf16, rows may be strided; weight: H; residual, sum_out: T x H of one dtype, either
     may be None; out: T x H bf16, fp32 or float8_e4m3fn, the last with fp32 scales: T x 1 (one per row) or
     T x ceil(H / 128) (one per 128 columns)."""
-    torch = _torch()
-    dev = _current_device(x, "x")
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    th = _torch()
+    dev = _current_device(th, x, "x")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("x must be T x H with contiguous rows")
-    T, H = x.shape
+    T, H = shape
     r = residual if residual is not None else sum_out
-    r_type = r.dtype if r is not None else x.dtype
-    if out.dtype == torch.float8_e4m3fn:
+    x_type, w_type, out_type = x.dtype, weight.dtype, out.dtype
+    r_type = r.dtype if r is not None else x_type
+    if out_type is th.f8:
         if scales is None or scales.dim() != 2:
             raise ValueError("an 8-bit output needs scales of T x 1 or T x ceil(H / 128)")
         out_code, block = SGT_F8E4M3, 0 if scales.shape[1] == 1 else 128
         s_shape = (T, 1 if block == 0 else -(-H // 128))
     else:
-        out_code, block, s_shape = _code(out.dtype), 0, None
-    _check(lib().sgt_rms_norm(x.data_ptr(), _code(x.dtype), x.stride(0) if T > 1 else max(H, 1),
-                              _layer_ptr(residual, "residual", r_type, (T, H), dev),
-                              _layer_ptr(sum_out, "sum_out", r_type, (T, H), dev),
-                              SGT_BF16 if r_type == torch.bfloat16 else SGT_F32,
-                              _layer_ptr(weight, "weight", weight.dtype, (H,), dev), _code(weight.dtype),
-                              _layer_ptr(out, "out", out.dtype, (T, H), dev), out_code,
-                              _layer_ptr(scales, "scales", torch.float32, s_shape, dev), block, T, H, eps,
-                              _layer_stream(stream, dev)))
+        out_code, block, s_shape = _code(th, out_type), 0, None
+    _check(lib().sgt_rms_norm(x.data_ptr(), _code(th, x_type), stride[0] if T > 1 else max(H, 1),
+                              _layer_ptr(residual, "residual", r_type, shape, dev),
+                              _layer_ptr(sum_out, "sum_out", r_type, shape, dev), _code(th, r_type),
+                              _layer_ptr(weight, "weight", w_type, (H,), dev), _code(th, w_type),
+                              _layer_ptr(out, "out", out_type, shape, dev), out_code,
+                              _layer_ptr(scales, "scales", th.f32, s_shape, dev), block, T, H, eps,
+                              _layer_stream(th, stream, dev)))
 
 
 def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_group: int = 1, topk_group: int = 1,
@@ -401,51 +410,51 @@ def moe_gate(logits, topk_ids, gate, *, bias=None, score: str = "softmax", n_gro
     int32 and gate: T x k fp32, written, as a2a_dispatch and a2a_combine take them; bias: E fp32, added to the scores
     for the choice only; score: 'softmax' or 'sigmoid'; with n_group > 1 the experts come from the topk_group groups of
     largest sum of their group_top largest scores (with the bias)."""
-    torch = _torch()
-    dev = _current_device(logits, "logits")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    th = _torch()
+    dev = _current_device(th, logits, "logits")
+    shape, stride = logits.shape, logits.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("logits must be T x E with contiguous rows")
-    T, E = logits.shape
+    T, E = shape
     k = topk_ids.shape[1]
     if n_group == 1:
         group_top = 1
-    _check(lib().sgt_moe_gate(logits.data_ptr(), _code(logits.dtype), logits.stride(0) if T > 1 else max(E, 1),
-                              _layer_ptr(bias, "bias", torch.float32, (E,), dev),
-                              _layer_ptr(topk_ids, "topk_ids", torch.int32, (T, k), dev),
-                              _layer_ptr(gate, "gate", torch.float32, (T, k), dev), T, E, k, SCORES[score], n_group,
-                              topk_group, group_top, 1 if renormalize else 0, scale, _layer_stream(stream, dev)))
+    _check(lib().sgt_moe_gate(logits.data_ptr(), _code(th, logits.dtype), stride[0] if T > 1 else max(E, 1),
+                              _layer_ptr(bias, "bias", th.f32, (E,), dev),
+                              _layer_ptr(topk_ids, "topk_ids", th.i32, (T, k), dev),
+                              _layer_ptr(gate, "gate", th.f32, (T, k), dev), T, E, k, SCORES[score], n_group,
+                              topk_group, group_top, 1 if renormalize else 0, scale, _layer_stream(th, stream, dev)))
 
 
-def _heads(t, name: str, dev):
+def _heads(th: _Torch, t, name: str, dev):
     """(pointer, token stride, head stride) of a bf16 tokens x heads x D tensor with contiguous heads."""
-    torch = _torch()
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not th.bf16:
         raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
     if t.get_device() != dev:
         raise ValueError("%s is on %s, expected GPU %d" % (name, t.device, dev))
-    st = t.stride()
+    st, shape = t.stride(), t.shape
     if len(st) != 3 or st[2] != 1:
         raise ValueError("%s must be tokens x heads x D with contiguous heads" % name)
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else 0, st[1] if t.shape[1] > 1 else 0
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
 
 
 def attn_prompt(q, k, v, out, cu_q, cu_k, *, lse=None, causal: bool = True, scale: Optional[float] = None, stream=None):
     """Attention over packed prompts (sgt_attn_prompt).  q: total_q x Hq x D, k and v: total_k x Hkv x D, bf16, any
     token and head strides (slices of one QKV tensor can be passed); out: total_q x Hq x D bf16; cu_q, cu_k: int32
     offsets of the sequences (n_seqs + 1); lse: total_q x Hq fp32 or None; scale: 1 / sqrt(D) by default."""
-    torch = _torch()
-    dev = _current_device(q, "q")
-    qp, kp, vp = _heads(q, "q", dev), _heads(k, "k", dev), _heads(v, "v", dev)
+    th = _torch()
+    dev = _current_device(th, q, "q")
+    qp, kp, vp = _heads(th, q, "q", dev), _heads(th, k, "k", dev), _heads(th, v, "v", dev)
     total_q, Hq, D = q.shape
     total_k, Hkv = k.shape[0], k.shape[1]
     if k.shape != v.shape or k.shape[2] != D:
         raise ValueError("k %s and v %s do not match q %s" % (tuple(k.shape), tuple(v.shape), tuple(q.shape)))
     n = cu_q.shape[0] - 1
-    _check(lib().sgt_attn_prompt(*qp, *kp, *vp, _layer_ptr(out, "out", torch.bfloat16, (total_q, Hq, D), dev),
-                                 _layer_ptr(lse, "lse", torch.float32, (total_q, Hq), dev),
-                                 _layer_ptr(cu_q, "cu_q", torch.int32, (n + 1,), dev),
-                                 _layer_ptr(cu_k, "cu_k", torch.int32, (n + 1,), dev), n, total_q, total_k, Hq, Hkv, D,
-                                 1 if causal else 0, D ** -0.5 if scale is None else scale, _layer_stream(stream, dev)))
+    _check(lib().sgt_attn_prompt(*qp, *kp, *vp, _layer_ptr(out, "out", th.bf16, (total_q, Hq, D), dev),
+                                 _layer_ptr(lse, "lse", th.f32, (total_q, Hq), dev),
+                                 _layer_ptr(cu_q, "cu_q", th.i32, (n + 1,), dev),
+                                 _layer_ptr(cu_k, "cu_k", th.i32, (n + 1,), dev), n, total_q, total_k, Hq, Hkv, D,
+                                 1 if causal else 0, D ** -0.5 if scale is None else scale, _layer_stream(th, stream, dev)))
 
 
 def attn_decode_workspace(B: int, Hq: int, Hkv: int, D: int) -> int:
@@ -462,31 +471,32 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, workspace, *, l
     strided; k_cache, v_cache: n_pages x page_size x Hkv x D bf16 with the same strides (a transposed view of
     n_pages x Hkv x page_size x D can be passed); block_table: B x max_pages int32, rows may be strided; seq_lens: B
     int32; out: B x Hq x D bf16 or fp32; workspace: at least attn_decode_workspace(B, Hq, Hkv, D) bytes."""
-    torch = _torch()
-    dev = _current_device(q, "q")
-    q_ptr, q_stride, q_head = _heads(q, "q", dev)
+    th = _torch()
+    dev = _current_device(th, q, "q")
+    q_ptr, q_stride, q_head = _heads(th, q, "q", dev)
     B, Hq, D = q.shape
     if Hq > 1 and q_head != D:
         raise ValueError("the heads of q must lie side by side")
-    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+    if k_cache.dtype != th.bf16 or v_cache.dtype != th.bf16:
         raise TypeError("the caches must be bfloat16, got %s and %s" % (k_cache.dtype, v_cache.dtype))
     if k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise ValueError("the caches are on %s and %s, expected GPU %d" % (k_cache.device, v_cache.device, dev))
-    st = k_cache.stride()
-    if len(st) != 4 or st[3] != 1 or v_cache.stride() != st or v_cache.shape != k_cache.shape or k_cache.shape[3] != D:
+    st, shape = k_cache.stride(), k_cache.shape
+    if len(st) != 4 or st[3] != 1 or v_cache.stride() != st or v_cache.shape != shape or shape[3] != D:
         raise ValueError("k_cache and v_cache must be n_pages x page_size x Hkv x D with the same strides")
-    n_pages, page_size, Hkv = k_cache.shape[:3]
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or \
-            block_table.get_device() != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    n_pages, page_size, Hkv, _ = shape
+    shape, table = block_table.shape, block_table.stride()
+    if len(shape) != 2 or shape[0] != B or block_table.dtype is not th.i32 or block_table.get_device() != dev or \
+            (shape[1] > 1 and table[1] != 1):
         raise ValueError("block_table must be %d x max_pages int32 on GPU %d with contiguous rows" % (B, dev))
-    max_pages = block_table.shape[1]
+    max_pages = shape[1]
     _check(lib().sgt_attn_decode(q_ptr, q_stride, k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n_pages,
-                                 page_size, block_table.data_ptr(), block_table.stride(0) if B > 1 else max_pages,
-                                 max_pages, _layer_ptr(seq_lens, "seq_lens", torch.int32, (B,), dev),
-                                 _layer_ptr(out, "out", out.dtype, (B, Hq, D), dev), _code(out.dtype),
-                                 _layer_ptr(lse, "lse", torch.float32, (B, Hq), dev),
+                                 page_size, block_table.data_ptr(), table[0] if B > 1 else max_pages,
+                                 max_pages, _layer_ptr(seq_lens, "seq_lens", th.i32, (B,), dev),
+                                 _layer_ptr(out, "out", out.dtype, (B, Hq, D), dev), _code(th, out.dtype),
+                                 _layer_ptr(lse, "lse", th.f32, (B, Hq), dev),
                                  _layer_ptr(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.numel() * workspace.element_size(),
-                                 B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _layer_stream(stream, dev)))
+                                 B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, _layer_stream(th, stream, dev)))
 
 
 class Context:

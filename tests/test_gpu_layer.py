@@ -646,3 +646,32 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(sgt.SgtError, match="workspace"):
         sgt.attn_decode(q, cache, cache, ids, torch.zeros(4, dtype=torch.int32, device=DEV), torch.empty_like(q),
                         torch.zeros(0, dtype=torch.uint8, device=DEV))
+
+
+def test_binding_refuses_types_it_does_not_know():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
+    w, half = x[0], x.half()
+    for kw in (dict(residual=half), dict(sum_out=half), dict(residual=x, sum_out=x.float())):
+        with pytest.raises(TypeError):
+            sgt.rms_norm(x, w, torch.empty_like(x), **kw)
+    with pytest.raises(TypeError):
+        sgt.rms_norm(x, w.half(), torch.empty_like(x))
+    with pytest.raises(TypeError):
+        sgt.rms_norm(x, w, half)
+    ids, gate = torch.zeros(4, 8, dtype=torch.int32, device=DEV), torch.zeros(4, 8, device=DEV)
+    with pytest.raises(TypeError):
+        sgt.moe_gate(half, ids, gate)
+    with pytest.raises(TypeError, match="bias"):
+        sgt.moe_gate(x, ids, gate, bias=w)
+    q = x.view(4, 1, 64)
+    cache = torch.zeros(2, 16, 1, 64, dtype=torch.bfloat16, device=DEV)
+    work = torch.zeros(sgt.attn_decode_workspace(4, 1, 1, 64), dtype=torch.uint8, device=DEV)
+    lens = torch.zeros(4, dtype=torch.int32, device=DEV)
+    with pytest.raises(TypeError):
+        sgt.attn_decode(q, cache, cache, ids, lens, q.half(), work)
+    with pytest.raises(TypeError, match="caches"):
+        sgt.attn_decode(q, cache.half(), cache.half(), ids, lens, torch.empty_like(q), work)
+    with pytest.raises(ValueError, match="block_table"):
+        sgt.attn_decode(q, cache, cache, ids.long(), lens, torch.empty_like(q), work)
+    with pytest.raises(ValueError, match="contiguous"):
+        sgt.rms_norm(x, w, torch.empty(64, 4, dtype=torch.bfloat16, device=DEV).t())
