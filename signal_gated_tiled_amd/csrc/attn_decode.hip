@@ -69,12 +69,11 @@ template <int kD> __device__ __forceinline__ int v_swz(int row) {
   return kD == 128 ? (row & 7) << 1 : ((row >> 1) & 3) << 1;
 }
 
-template <int kT>
-__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int64_t room) {
-  if (b >= a.B) return 0;
-  const int64_t n = min((int64_t)max(a.lens[b], 0), room);
-  return (int)max((n + kT - 1) / kT, (int64_t)1);   // an empty sequence is one tile of unseen keys
+// Keys of sequence b, -1 past the last one; and the tiles of so many keys (an empty sequence is one tile of unseen keys).
+__device__ __forceinline__ int keys_of(const DecodeArgs& a, int b, int room) {
+  return b < a.B ? min(max(a.lens[b], 0), room) : -1;
 }
+template <int kT> __device__ __forceinline__ int tiles_of(int keys) { return keys < 0 ? 0 : max((int)(((int64_t)keys + kT - 1) / kT), 1); }
 
 // x / y of values that rarely need their upper halves.
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
@@ -125,23 +124,24 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   __shared__ __attribute__((aligned(1024))) Stage sA[kWaves], sB[kWaves], sC[kWaves], sD[kWaves];
   __shared__ int64_t sRow[kWaves][64];             // byte offsets in the cache of the rows of kGroup tiles
   __shared__ float sM[kWaves][kMaxRows], sL[kWaves][kMaxRows];
-  __shared__ int64_t red[kWaves], found[2];
+  __shared__ int64_t red[kWaves], found[3];
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), g = lane >> 4, col = lane & 15;
   const int G = a.Hq / a.Hkv, HC = a.Hkv * chunks;
-  const int64_t room = (int64_t)a.max_pages * a.page_size;
+  const int room = a.max_pages * a.page_size;   // (below 2^31)
 
   // this workgroup's range of the units (of each problem its tiles, then its cost)
   int64_t total = 0, end0 = 0, total0 = 0;   // end0, total0: of the first kThreads sequences
-  int cost0 = 0;
+  int cost0 = 0, keys0 = -1;
   for (int c = 0; c < a.B; c += kThreads) {
-    const int n = tiles_of<kT>(a, c + tid, room), cost = n > 0 ? n + kProblemCost : 0;
+    const int keys = keys_of(a, c + tid, room), cost = keys >= 0 ? tiles_of<kT>(keys) + kProblemCost : 0;
     int64_t t;
     const int64_t end = block_scan(cost, red, &t);
     if (c == 0) {
       end0 = end;
       total0 = t;
       cost0 = cost;
+      keys0 = keys;
     }
     total += t;
   }
@@ -152,16 +152,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   if (u0 >= units) return;
   for (int64_t c = 0, before = 0; c < a.B; c += kThreads) {
     int64_t end = end0, t = total0;
-    int cost = cost0;
+    int cost = cost0, keys = keys0;
     if (c > 0) {
-      const int n = tiles_of<kT>(a, (int)c + tid, room);
-      cost = n > 0 ? n + kProblemCost : 0;
+      keys = keys_of(a, (int)c + tid, room);
+      cost = keys >= 0 ? tiles_of<kT>(keys) + kProblemCost : 0;
       end = block_scan(cost, red, &t);
     }
     end += before;
     if (cost > 0 && (end - cost) * HC <= u0 && u0 < end * HC) {
       found[0] = c + tid;
       found[1] = end - cost;
+      found[2] = keys;
     }
     before += t;
     if (before * HC > u0) break;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   __syncthreads();
   int b = uniform((int)found[0]);
   int64_t start = uniform(found[1]) * HC;   // first unit of the problem
-  int n_tiles = tiles_of<kT>(a, b, room);
+  int n_keys = uniform((int)found[2]), n_tiles = tiles_of<kT>(n_keys);
   int hc = (int)quotient(u0 - start, n_tiles + kProblemCost);
   start += (int64_t)hc * (n_tiles + kProblemCost);
 
@@ -179,11 +180,24 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
 
   auto problem = [&](int ta, int tb) {   // its tiles ta .. tb - 1
     const int hk = hc / chunks, h0 = hk * G + (hc % chunks) * kQ, nh = min(kQ, (hk + 1) * G - h0);
-    const int n_keys = (int)min((int64_t)max(a.lens[b], 0), room);
     // (an empty sequence's row is never looked at; any readable word will do)
     const int32_t* table = n_keys > 0 ? a.table + (int64_t)b * a.table_stride : a.lens;
     const int64_t head_off = hk * a.head_stride;
 
+    // this wave's tiles are ta + w, ta + w + 4, ...: nt of them
+    const int nt = (tb - ta - w + kWaves - 1) / kWaves;
+    auto key_of = [&](int group) {   // this lane's key of the group; past the last tile, that tile's again
+      return (ta + w + kWaves * min(group * kGroup + lane / kT, nt - 1)) * kT + lane % kT;
+    };
+    auto page_of = [&](int group) {
+      const int key = key_of(group);
+      return table[key < n_keys ? key / a.page_size : 0];
+    };
+    // page ids before the queries, so that the first tiles' addresses wait for nothing else
+    int page[kPages];
+#pragma unroll
+    for (int i = 0; i < kPages; ++i) page[i] = nt > 0 ? page_of(i) : -1;
+    asm volatile("" ::: "memory");
     bf16x8_t q[kNQ][kD / 32];
 #pragma unroll
     for (int i = 0; i < kNQ; ++i)
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
         u32x4_t v = {0, 0, 0, 0};
         if (16 * i + col < nh)
           v = *(const u32x4_t*)(a.q + b * a.q_stride + (int64_t)(h0 + 16 * i + col) * kD + 32 * s + 8 * g);
-        q[i][s] = __builtin_bit_cast(bf16x8_t, v ^ u32x4_t{sign, sign, sign, sign});
+        q[i][s] = __builtin_bit_cast(bf16x8_t, v);
       }
     f32x4_t o[kNQ][kNB];
     float m[kNQ], mc[kNQ], lim[kNQ], l[kNQ];
@@ -204,15 +218,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       for (int n = 0; n < kNB; ++n) o[i][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    // this wave's tiles are ta + w, ta + w + 4, ...: nt of them
-    const int nt = (tb - ta - w + kWaves - 1) / kWaves;
-    auto key_of = [&](int group) {   // this lane's key of the group; past the last tile, that tile's again
-      return (ta + w + kWaves * min(group * kGroup + lane / kT, nt - 1)) * kT + lane % kT;
-    };
-    auto page_of = [&](int group) {
-      const int key = key_of(group);
-      return table[key < n_keys ? key / a.page_size : 0];
-    };
     // Lay out the rows of a group for its loads; returns which of its keys are seen, a bit for each lane.
     auto rows = [&](int group, int page) {
       const int key = key_of(group);
@@ -314,10 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
     };
 
     if (nt > 0) {
-      int page[kPages];
       uint64_t cur[kPages], next[kPages];
-#pragma unroll
-      for (int i = 0; i < kPages; ++i) page[i] = page_of(i);
       auto issue = [&](int j, int i, uint64_t& seen, Stage& st) {   // tile j + i; i is a constant
         if (i % kGroup == 0) {
           const int group = (j + i) / kGroup;
@@ -329,6 +331,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       issue(0, 0, cur[0], sA[w]);
       issue(0, 1, cur[1 / kGroup % kPages], sB[w]);
       issue(0, 2, cur[2 / kGroup % kPages], sC[w]);
+      __builtin_amdgcn_sched_barrier(0);   // the queries are waited for here, not before the loads
+#pragma unroll
+      for (int i = 0; i < kNQ; ++i)
+#pragma unroll
+        for (int s = 0; s < kD / 32; ++s)
+          q[i][s] = __builtin_bit_cast(bf16x8_t, __builtin_bit_cast(u32x4_t, q[i][s]) ^ u32x4_t{sign, sign, sign, sign});
       auto step = [&](int j, int i, Stage& st, Stage& free) {       // tile j + i; i is a constant
         wait_vm<2 * 2 * kDma>();
         issue(j, i + 3, next[(i + 3) / kGroup % kPages], free);
@@ -431,11 +439,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
         return last != 0;
       };
       const __amdgpu_buffer_rsrc_t ra = make_rsrc(parts, (uint64_t)kGrid * 2 * kSlotFloats * 4);
+      // (No acquire: these loads go past the caches that are not coherent, as the stores did, and are issued after the count.)
       // Join n parts first, first + by, ..., whose maxima and sums lie at `stats`: into the first one's slot, or the result.
       // kAtOnce >= n of them are loaded together.
       auto join = [&](auto at_once, int first, int by, int n, int stats, bool result) {
         constexpr int kAtOnce = decltype(at_once)::value;
-        acquire_agent();
         for (int e = jt; e < nh * kD / 4; e += kThreads) {
           const int r = e / (kD / 4), at = e % (kD / 4);
           auto off = [&](int i, int f) {   // past the last part: out of the buffer's range, which reads as 0
@@ -492,7 +500,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
     if (start >= u1) break;
     if (++hc == HC) {
       hc = 0;
-      n_tiles = tiles_of<kT>(a, ++b, room);
+      n_keys = keys_of(a, ++b, room);
+      n_tiles = tiles_of<kT>(n_keys);
     }
   }
 }
