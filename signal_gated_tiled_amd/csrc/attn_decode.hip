@@ -75,9 +75,32 @@ __device__ __forceinline__ int keys_of(const DecodeArgs& a, int b, int room) {
 }
 template <int kT> __device__ __forceinline__ int tiles_of(int keys) { return keys < 0 ? 0 : max((int)(((int64_t)keys + kT - 1) / kT), 1); }
 
-// x / y of values that rarely need their upper halves.
+// x / y of values that rarely need their upper halves (then bit by bit: what matters is little code, since a short call
+// waits for its instructions more than for their results).
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  return ((uint64_t)(x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+  if (((uint64_t)(x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
+  uint64_t q = 0, r = 0;
+#pragma unroll 1
+  for (int i = 63; i >= 0; --i) {
+    r = r << 1 | ((uint64_t)x >> i & 1);
+    q = q << 1 | (r >= (uint64_t)y);
+    if (q & 1) r -= (uint64_t)y;
+  }
+  return (int64_t)q;
+}
+
+// Division by d of numbers below 2^31, exactly: n / d = n m >> s with s = 31 + ceil(log2 d) and m = ceil(2^s / d), which
+// has 32 bits (m d - 2^s < d <= 2^(s - 31), so that the error n (m d - 2^s) / (d 2^s) is below 1 / d).
+struct Divisor {
+  uint32_t m;
+  int32_t s, d;
+  __device__ __forceinline__ int operator()(int n) const { return (int)((uint64_t)(uint32_t)n * m >> s); }
+};
+Divisor divisor(int d) {
+  int s = 31;
+  while ((1ll << (s - 31)) < d) ++s;
+  const unsigned __int128 two = (unsigned __int128)1 << s;
+  return {(uint32_t)((two + d - 1) / d), s, d};
 }
 
 // Inclusive prefix sum over the workgroup and its total; `red` holds kWaves words.
@@ -110,7 +133,8 @@ __device__ __forceinline__ int fresh_lane() {
 }
 
 template <int kD, int kNQ>
-__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, int chunks, float* parts, uint32_t* counters) {
+__global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, Divisor chunks, Divisor page_size, float* parts,
+                                                                  uint32_t* counters) {
   constexpr int kT = tile_keys<kD>();              // keys per tile
   constexpr int kTile = kT * kD * 2;               // bytes of a tile of keys or values: 4 KiB
   constexpr int kDma = kTile / 1024;               // 1 KiB DMA loads of each
@@ -127,9 +151,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   __shared__ int64_t red[kWaves], found[3];
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), g = lane >> 4, col = lane & 15;
-  const int G = a.Hq / a.Hkv, HC = a.Hkv * chunks;
+  const int G = a.G, HC = a.Hkv * chunks.d;
   const int room = a.max_pages * a.page_size;   // (below 2^31)
 
+  // one argument of every cache line: their misses then overlap, instead of each being met where its arguments are used
+  asm volatile("" ::"s"(a.q), "s"(a.workspace), "s"(a.n_pages), "s"(a.scale), "s"(page_size.m), "s"(counters));
   // this workgroup's range of the units (of each problem its tiles, then its cost)
   int64_t total = 0, end0 = 0, total0 = 0;   // end0, total0: of the first kThreads sequences
   int cost0 = 0, keys0 = -1;
@@ -179,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
   const gptr_t gk = (gptr_t)a.k, gv = (gptr_t)a.v;
 
   auto problem = [&](int ta, int tb) {   // its tiles ta .. tb - 1
-    const int hk = hc / chunks, h0 = hk * G + (hc % chunks) * kQ, nh = min(kQ, (hk + 1) * G - h0);
+    const int hk = uniform(chunks(hc)), h0 = hk * G + (hc - hk * chunks.d) * kQ, nh = min(kQ, (hk + 1) * G - h0);
     // (an empty sequence's row is never looked at; any readable word will do)
     const int32_t* table = n_keys > 0 ? a.table + (int64_t)b * a.table_stride : a.lens;
     const int64_t head_off = hk * a.head_stride;
@@ -191,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
     };
     auto page_of = [&](int group) {
       const int key = key_of(group);
-      return table[key < n_keys ? key / a.page_size : 0];
+      return table[key < n_keys ? page_size(key) : 0];
     };
     // page ids before the queries, so that the first tiles' addresses wait for nothing else
     int page[kPages];
@@ -223,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       const int key = key_of(group);
       const bool valid = key < n_keys && page >= 0 && page < a.n_pages;
       // a row that is not seen reads the cache's first row instead; what that holds is masked
-      const int64_t p = valid ? page : 0, slot = valid ? key % a.page_size : 0;
+      const int64_t p = valid ? page : 0, slot = valid ? key - page_size(key) * page_size.d : 0;
       sRow[w][lane] = 2 * (head_off + p * a.page_stride + slot * a.slot_stride);
       __builtin_amdgcn_wave_barrier();
       return (uint64_t)__ballot(valid);
@@ -372,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
     // join the waves: each scales its output to the common maximum and leaves it in its stage
     const int jl = fresh_lane(), jt = w * 64 + jl, jg = jl >> 4, jc = jl & 15;
     const bool whole = ta == 0 && tb == n_tiles;
-    const int64_t w_first = quotient(start, chunk);
+    const int64_t w_first = start >= u0 ? (int64_t)blockIdx.x : quotient(start, chunk);
     const bool inside = start != w_first * chunk;   // the problem starts inside a range: that part has the second slot
     const int64_t slot = blockIdx.x * 2 + (blockIdx.x == w_first && inside ? 1 : 0);
     float* part = parts + slot * kSlotFloats;
@@ -518,7 +544,7 @@ hipError_t launch(const DecodeArgs& a, hipStream_t stream) {
   const int64_t grid = min((int64_t)kGrid, (most + kMinTiles - 1) / kMinTiles);
   float* parts = static_cast<float*>(a.workspace);
   attn_decode_kernel<kD, kNQ><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(
-      a, chunks, parts, reinterpret_cast<uint32_t*>(static_cast<char*>(a.workspace) + kPartBytes));
+      a, divisor(chunks), divisor(a.page_size), parts, reinterpret_cast<uint32_t*>(static_cast<char*>(a.workspace) + kPartBytes));
   return hipGetLastError();
 }
 

@@ -58,7 +58,7 @@ struct DecodeArgs {
   void* workspace;
   int64_t q_stride, page_stride, slot_stride, head_stride, table_stride;
   int64_t n_pages;
-  int32_t B, Hq, Hkv, D;
+  int32_t B, Hq, Hkv, G, D;   // G = Hq / Hkv
   int32_t page_size, max_pages, out_f32;
   float scale;
 };

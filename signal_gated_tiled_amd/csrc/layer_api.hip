@@ -171,7 +171,7 @@ sgt_status sgt_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
   a.v = static_cast<const uint16_t*>(v_cache); a.table = block_table; a.lens = seq_lens; a.out = out; a.lse = lse;
   a.workspace = workspace; a.q_stride = q_stride; a.page_stride = page_stride; a.slot_stride = slot_stride;
   a.head_stride = head_stride; a.table_stride = table_stride; a.n_pages = n_pages;
-  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.page_size = page_size; a.max_pages = n_pages > 0 ? max_pages : 0;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.D = D; a.page_size = page_size; a.max_pages = n_pages > 0 ? max_pages : 0;
   a.out_f32 = out_dtype == SGT_F32; a.scale = scale;
   HIP_TRY(launch_attn_decode(a, static_cast<hipStream_t>(stream)));
   return SGT_OK;
