@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
 
   const float c = weight_exponent(a.scale);
   bf16x8_t q[kD / 16];
-  {
+  auto load_q = [&] {
     const uint16_t* p = a.q + (t.q0 + token) * a.q_token + head * a.q_head + 8 * half;
     const uint32_t sign = query_sign(a.scale);
 #pragma unroll
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
       if (valid) v = *reinterpret_cast<const u32x4_t*>(p + 16 * i);
       q[i] = __builtin_bit_cast(bf16x8_t, v ^ u32x4_t{sign, sign, sign, sign});
     }
-  }
+  };
   // this lane's first chunk of a K row and of a V row in LDS; product step t of the scores lies 2 t chunks on, column block
   // b of V 4 b chunks on, both under the swizzle, so that one xor moves there
   const uint32_t ka0 = (uint32_t)((lane & 31) * kD * 2 + ((half ^ k_swz<kD>(lane & 31)) << 4));
@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
     st.l = st.mc = 0.f;
     if (tiles == 0) return;
     kd.issue(sK0, 0);
+    if (!again) load_q();   // (on their way together)
     kd.issue(sK1, kKeys);
     vd.issue(sV0, 0);
     if constexpr (kRing == 4) {
@@ -510,101 +511,122 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
     }
     wait_vm<0>();   // no load may land in the stages after this
   };
-  // The key groups' parts of each row, brought to their common maximum and added: key group 0 holds the row.
+  // The key groups' parts of each row, brought to their common maximum and added.  Every wave leaves its whole part in LDS
+  // and adds up one slice of its rows' columns: accumulator registers kg kR .. kg kR + kR - 1 of all key groups.
+  constexpr int kR = kD / 2 / kS, kBox = kD * 128;   // registers of a slice, bytes of a part
+  float res[kS > 1 ? kR : 1];
+  auto box_of = [&](int x) {
+    uint8_t* p = x < 2 ? sK0 : x < 4 ? sK1 : x < 6 ? sV0 : sV1;
+    return reinterpret_cast<f32x4_t*>(p + (x & 1) * kBox) + lane;
+  };
   auto join = [&] {
     if constexpr (kS > 1) {
+      static_assert(2 * kBox <= kTileBytes, "two parts in each stage");
       st.l += other_half(st.l);
-      const float own = st.m == -INFINITY ? -INFINITY : st.mc;
       __syncthreads();                    // all reads of the stages are done
-      sM[w][lane & 31] = own;
+      f32x4_t* box = box_of(w);
+#pragma unroll
+      for (int i = 0; i < kD / 8; ++i)
+        box[i * 64] = f32x4_t{st.o[i / 4][i % 4 * 4], st.o[i / 4][i % 4 * 4 + 1], st.o[i / 4][i % 4 * 4 + 2], st.o[i / 4][i % 4 * 4 + 3]};
+      sM[w][lane & 31] = st.m == -INFINITY ? -INFINITY : st.mc;
+      sL[w][lane & 31] = st.l;
       __syncthreads();
-      float m = -INFINITY;
+      float m = -INFINITY, f[kS];
 #pragma unroll
-      for (int g = 0; g < kS; ++g) m = fmaxf(m, sM[g * kRowWaves + rw][lane & 31]);
-      const float f = own == -INFINITY ? (st.l == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(own - m);
+      for (int g = 0; g < kS; ++g) {
+        f[g] = sM[g * kRowWaves + rw][lane & 31];
+        m = fmaxf(m, f[g]);
+      }
       st.mc = m == -INFINITY ? 0.f : m;
-      st.l *= f;
+      st.l = 0.f;
 #pragma unroll
-      for (int b = 0; b < kD / 32; ++b)
+      for (int g = 0; g < kS; ++g) {
+        const float l = sL[g * kRowWaves + rw][lane & 31];
+        f[g] = f[g] == -INFINITY ? (l == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(f[g] - m);
+        st.l += l * f[g];
+      }
 #pragma unroll
-        for (int r = 0; r < 16; ++r) st.o[b][r] *= f;
+      for (int g = 0; g < kS; ++g) {
+        const f32x4_t* part = box_of(g * kRowWaves + rw) + kg * (kR / 4) * 64;
 #pragma unroll
-      for (int n = kS / 2; n >= 1; n /= 2) {   // groups n .. 2 n - 1 go to groups 0 .. n - 1
-        const int at = kg % n * kRowWaves + rw;
-        f32x4_t* box = reinterpret_cast<f32x4_t*>(at == 0 ? sK0 : at == 1 ? sK1 : at == 2 ? sV0 : sV1) + lane;
-        if (kg >= n && kg < 2 * n) {
+        for (int i = 0; i < kR; i += 4) {
+          const f32x4_t x = part[i / 4 * 64];
 #pragma unroll
-          for (int b = 0; b < kD / 32; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4)
-              box[(4 * b + r / 4) * 64] = f32x4_t{st.o[b][r], st.o[b][r + 1], st.o[b][r + 2], st.o[b][r + 3]};
-          sL[at][lane & 31] = st.l;
+          for (int e = 0; e < 4; ++e) res[i + e] = g == 0 ? x[e] * f[0] : __builtin_fmaf(x[e], f[g], res[i + e]);
         }
-        __syncthreads();
-        if (kg < n) {
-#pragma unroll
-          for (int b = 0; b < kD / 32; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-              const f32x4_t x = box[(4 * b + r / 4) * 64];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) st.o[b][r + i] += x[i];
-            }
-          st.l += sL[at][lane & 31];
-        }
-        __syncthreads();
       }
       st.l = half == 0 ? st.l : 0.f;      // the halves are added once more below
     }
   };
+  auto value = [&](int i) -> float {      // register i of this wave's slice
+    if constexpr (kS > 1) return res[i];
+    else return st.o[i / 16][i % 16];
+  };
   pass(false);
   join();
-  auto non_finite = [&] {
+  bool bad = false;
+  {
     float top = 0.f;
 #pragma unroll
-    for (int b = 0; b < kD / 32; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = abs_max(top, st.o[b][r]);
+    for (int i = 0; i < kR; ++i) top = abs_max(top, value(i));
     top = abs_max(top, other_half(top));
-    return valid && kg == 0 && !(top < INFINITY);
-  };
-  const bool bad = non_finite();
-  bool done = !valid || kg > 0;
+    bad = valid && !(top < INFINITY);
+  }
+  bool done = !valid;
   if (__syncthreads_or(bad)) {
+    // whether any of the waves that share this wave's rows says so
+    auto any_wave = [&](bool mine) {
+      if constexpr (kS > 1) {
+        __syncthreads();
+        sM[w][lane & 31] = mine ? 1.f : 0.f;
+        __syncthreads();
+#pragma unroll
+        for (int g = 0; g < kS; ++g) mine |= sM[g * kRowWaves + rw][lane & 31] != 0.f;
+      }
+      return mine;
+    };
+    bad = any_wave(bad);
     __syncthreads();
     pass(true);
     join();
     // rows that were not finite: by plain loops, kept where the row itself sees such a value
-    uint64_t todo = __ballot(bad) & 0xFFFFFFFFull;
+    uint64_t todo = kg == 0 ? __ballot(bad) & 0xFFFFFFFFull : 0;
     while (todo) {
       const int i = __ffsll((unsigned long long)todo) - 1;
       todo &= todo - 1;
       const int rr = w_first + i;
       if (plain_row<kD>(a, t.q0 + rr / G, hk * G + rr % G, hk, t.k0, limit_of(rr / G)) && (lane & 31) == i) done = true;
     }
+    done = any_wave(done);
   }
   if (done) return;
   const float l = st.l + other_half(st.l);
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int64_t at = (t.q0 + token) * a.Hq + head;
-  if (a.lse && half == 0) a.lse[at] = l == 0.f ? -INFINITY : (st.mc + __builtin_amdgcn_logf(l)) * kLn2;
+  if (a.lse && half == 0 && kg == 0) a.lse[at] = l == 0.f ? -INFINITY : (st.mc + __builtin_amdgcn_logf(l)) * kLn2;
   // two groups of 8 columns at a time: the lower half-wave ends up with the whole first group, the upper with the second
-  uint16_t* out = a.out + at * kD;
+  uint16_t* out = a.out + at * kD + kg * (2 * kR) * (kS > 1);
 #pragma unroll
-  for (int b = 0; b < kD / 32; ++b)
+  for (int i = 0; i < kR; i += 8) {
+    uint32_t x[2], y[2];
 #pragma unroll
-    for (int g = 0; g < 4; g += 2) {
-      uint32_t x[2], y[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[i] = pack_bf16(st.o[b][4 * g + 2 * i] * inv, st.o[b][4 * g + 2 * i + 1] * inv);
-        y[i] = pack_bf16(st.o[b][4 * g + 4 + 2 * i] * inv, st.o[b][4 * g + 4 + 2 * i + 1] * inv);
-      }
-      const auto e0 = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
-      const auto e1 = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
-      *reinterpret_cast<u32x4_t*>(out + 32 * b + 8 * (g + half)) = u32x4_t{e0[0], e1[0], e0[1], e1[1]};
+    for (int e = 0; e < 2; ++e) {
+      x[e] = pack_bf16(value(i + 2 * e) * inv, value(i + 2 * e + 1) * inv);
+      y[e] = pack_bf16(value(i + 4 + 2 * e) * inv, value(i + 4 + 2 * e + 1) * inv);
     }
+    const auto e0 = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
+    const auto e1 = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
+    *reinterpret_cast<u32x4_t*>(out + 2 * i + 8 * half) = u32x4_t{e0[0], e1[0], e0[1], e1[1]};
+  }
 }
+
+// (named, since the compiler leaves out the host's side of some of them otherwise)
+template __global__ void attn_prompt_kernel<64, 1>(PromptArgs);
+template __global__ void attn_prompt_kernel<64, 2>(PromptArgs);
+template __global__ void attn_prompt_kernel<64, 4>(PromptArgs);
+template __global__ void attn_prompt_kernel<128, 1>(PromptArgs);
+template __global__ void attn_prompt_kernel<128, 2>(PromptArgs);
+template __global__ void attn_prompt_kernel<128, 4>(PromptArgs);
 
 template <int kD, int kS>
 hipError_t launch(const PromptArgs& a, hipStream_t stream) {
