@@ -25,9 +25,9 @@
 //
 // Rounding.  Scores, maxima, sums, parts and joins are fp32; the weights are two bf16 parts (16 bits of each weight).
 //
-// Measured: 4 sequences of 90000 to 131072 tokens, 64 query heads on 8, D 128, 305 us (1.75 GB at 5.7 TB/s; a 2 GiB copy
-// reaches 4.9 here); 128 sequences of 1 to 16000, 8 heads on one, 33 us (117 MB at 3.5 TB/s, of which about 8 us are the chain of
-// launch, lengths, page ids, first tile and joins); one of 777 10.2 us, that chain alone.
+// Measured: 4 sequences of 90000 to 131072 tokens, 64 query heads on 8, D 128, 303 us (1.75 GB at 5.8 TB/s; a 2 GiB copy
+// reaches 4.9 here); 128 sequences of 1 to 16000, 8 heads on one, 32 us (117 MB at 3.6 TB/s, of which about 8 us are the chain of
+// launch, lengths, page ids, first tile and joins); one of 777 9.8 us, that chain alone.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -13,7 +13,7 @@
 // at the end, which costs one small gather instead of carrying every score along.
 //
 // Scores, sums and weights are fp32.  Measured: 16381 x 256 in groups with a bias 12.0 us (17.8 MB, 1.5 TB/s; about 1150
-// vector instructions per wave of four tokens, issued nearly without a gap), 16381 x 64 softmax 4.9, 16 tokens 3.3: the
+// vector instructions per wave of four tokens, on which the vector units spend some 9 of them), 16381 x 64 softmax 4.9, 16 tokens 3.3: the
 // launch, two memory latencies and eight dependent rounds.
 #include <hip/hip_runtime.h>
 
