@@ -18,7 +18,7 @@
 // both operands agree, and V^T is read out of the row-major V tile in that
 // order by the transposing LDS read (four keys of one column per lane).
 //
-// LDS.  K and V tiles arrive by HBM-to-LDS DMA, in four stages each (two where a workgroup splits the keys): the loads of
+// LDS.  K and V tiles arrive by HBM-to-LDS DMA, in four stages each (two where D 128's keys are split): the loads of
 // the next tiles are in flight while tile j is computed.  16-byte chunk c of row r is stored at chunk c ^ swizzle(r), so that
 // the 16 lanes of a read touch all banks (no conflicts counted).
 //
@@ -30,7 +30,7 @@
 // Measured: one causal prompt of 16384 tokens, 8 query heads on one key head, D 128, 495 us (1.1 PFLOP/s; a large matrix
 // product of this card's library reaches 1.5), matrix units busy 53% of the cycles, vector units 41%; 16 prompts of 1 to
 // 1500 tokens 31 us, bound by the longest one's chain of steps of about 1.7 us; 3 pieces of 300 to 700 tokens behind 6000,
-// 16 heads on 4, D 64, 79 us (0.57 PFLOP/s: half the matrix work per exponential).
+// 16 heads on 4, D 64, 76 us (0.60 PFLOP/s: half the matrix work per exponential).
 //
 // Values of keys a row does not see get weight 0, which a NaN or infinity
 // would survive.  Keys past a sequence's end read as zeros; a later key inside
@@ -390,7 +390,9 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
   constexpr int kW = 8, kRowWaves = kW / kS, kRows = 32 * kRowWaves;
   constexpr int kB = kS == 4 ? 1 : 2;             // 32-key blocks of a wave's part of a tile
   constexpr int kPart = 32 * kB, kKeys = kPart * kS;
-  constexpr int kRing = kS == 1 ? 4 : 2;          // stages of a tile of keys, and of values
+  // Stages of a tile of keys, and of values: four where the LDS holds them (3 pieces behind 6000 tokens at D 64 75.8 us,
+  // with two 79.6; 64 tokens behind 4000 32.8 and 35.4).
+  constexpr int kRing = kKeys * kD <= 8192 ? 4 : 2;
   constexpr int kTileBytes = kKeys * kD * 2, kExtra = kRing == 4 ? kTileBytes : 16;
   // distinct objects, so that the compiler knows that a DMA into one is not read through another
   __shared__ __attribute__((aligned(1024))) uint8_t sK0[kTileBytes], sK1[kTileBytes], sK2[kExtra], sK3[kExtra];
