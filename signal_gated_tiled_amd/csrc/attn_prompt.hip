@@ -27,10 +27,10 @@
 //
 // What bounds it: a wave's step of 64 keys at D 128 is 32 matrix instructions (1024 cycles) beside about 170 vector
 // instructions (32 exponentials of 8 cycles, 16 packings of 8, the rest 3 to 5), and with long prompts the power limit.
-// Measured: one causal prompt of 16384 tokens, 8 query heads on one key head, D 128, 495 us (1.1 PFLOP/s; a large matrix
+// Measured: one causal prompt of 16384 tokens, 8 query heads on one key head, D 128, 489 us (1.1 PFLOP/s; a large matrix
 // product of this card's library reaches 1.5), matrix units busy 53% of the cycles, vector units 41%; 16 prompts of 1 to
-// 1500 tokens 31 us, bound by the longest one's chain of steps of about 1.7 us; 3 pieces of 300 to 700 tokens behind 6000,
-// 16 heads on 4, D 64, 76 us (0.60 PFLOP/s: half the matrix work per exponential).
+// 1500 tokens 29 us, bound by the longest one's chain of steps of about 1.6 us; 3 pieces of 300 to 700 tokens behind 6000,
+// 16 heads on 4, D 64, 72 us (0.64 PFLOP/s: half the matrix work per exponential).
 //
 // Values of keys a row does not see get weight 0, which a NaN or infinity
 // would survive.  Keys past a sequence's end read as zeros; a later key inside
@@ -473,11 +473,17 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
       u32x4_t p[4];
       bf16x8_t k[2][kB], v[2][kD / 32];
       uint32_t ka = ka0, va = va0;
-      asm volatile("" : "+v"(ka), "+v"(va));   // the xors stay here: twelve addresses kept over the loop would spill
+      // (D 128: the xors stay here, since twelve addresses kept over the loop would spill)
+      if constexpr (kD == 128) asm volatile("" : "+v"(ka), "+v"(va));
       read_k<kD, kB>(K1 + part, ka, 0, k[0]);
       __builtin_amdgcn_sched_barrier(0);
       // (past the last tile: zeros' scores, not used)
+      // Raised priority: of a SIMD's two waves the one that weighs, whose vector instructions fill the gaps between matrix
+      // instructions, goes before the one that multiplies, which waits for the matrix unit anyway (3 pieces behind 6000 tokens at
+      // D 64 75.8 -> 72.4 us, 16 prompts of 300 to 1500 51.6 -> 48.7, 16384 tokens 498 -> 489; raised for the products: none).
+      __builtin_amdgcn_s_setprio(1);
       scores_and_weights<kD, kB>(K1 + part, V0 + part, q, ka, va, nxt, cur, st, top, c, p, k, v, loads);
+      __builtin_amdgcn_s_setprio(0);
       const int next = j0 + kKeys + mine;
       if (next + kPart > w_all) mask_scores<kB>(nxt, my_seen - next);
       __builtin_amdgcn_sched_barrier(0);
@@ -642,8 +648,9 @@ template <int kD>
 hipError_t launch_dim(const PromptArgs& a, hipStream_t stream) {
   // Tiles of 256 rows, against 256 CUs of one workgroup each: where they do not fill the chip, the keys are split over a
   // workgroup's waves instead of more rows.  Measured, one causal prompt of 8 query heads and 1 key head, D 128
-  // (us at 1 / 2 / 4 key groups): 2048 tokens (64 tiles) 56 / 37 / 30, 4096 (128) 102 / 65 / 65, 8192 (256) 201 / 155 / 202,
-  // 12000 (375) 329 / 332 / 399, 16384 (512) 558 / 573 / 702; 16 prompts of 1 to 1500 tokens (134) 53 / 34 / 46.
+  // (us at 1 / 2 / 4 key groups): 2048 tokens (64 tiles) 51 / 34 / 30, 4096 (128) 92 / 59 / 66, 8192 (256) 187 / 142 / 220,
+  // 12000 (375) 310 / 307 / 453, 16384 (512) 491 / 526 / 819; 16 prompts of 1 to 1500 tokens (134) 45 / 29 / 40, of 300 to 1500
+  // (375) 49 / 58 / 95.
   const int64_t tiles = a.total_q * a.Hq / 256;
   if (tiles >= 320) return launch<kD, 1>(a, stream);
   if (tiles >= 96) return launch<kD, 2>(a, stream);
