@@ -18,7 +18,7 @@
 // both operands agree, and V^T is read out of the row-major V tile in that
 // order by the transposing LDS read (four keys of one column per lane).
 //
-// LDS.  K and V tiles arrive by HBM-to-LDS DMA, in four stages each (two where D 128's keys are split): the loads of
+// LDS.  K and V tiles arrive by HBM-to-LDS DMA, in two to eight stages each: the loads of
 // the next tiles are in flight while tile j is computed.  16-byte chunk c of row r is stored at chunk c ^ swizzle(r), so that
 // the 16 lanes of a read touch all banks (no conflicts counted).
 //
@@ -390,13 +390,15 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
   constexpr int kW = 8, kRowWaves = kW / kS, kRows = 32 * kRowWaves;
   constexpr int kB = kS == 4 ? 1 : 2;             // 32-key blocks of a wave's part of a tile
   constexpr int kPart = 32 * kB, kKeys = kPart * kS;
-  // Stages of a tile of keys, and of values: four where the LDS holds them (3 pieces behind 6000 tokens at D 64 75.8 us,
-  // with two 79.6; 64 tokens behind 4000 32.8 and 35.4).
-  constexpr int kRing = kKeys * kD <= 8192 ? 4 : 2;
-  constexpr int kTileBytes = kKeys * kD * 2, kExtra = kRing == 4 ? kTileBytes : 16;
+  // Stages of a tile of keys, and of values: as many as the LDS holds, since half as many steps pass between barriers.  (D 64,
+  // 16384 tokens of 8 heads on 1: eight 293 us, four 301; 3 pieces behind 6000 tokens: four 75.8, two 79.6.)
+  constexpr int kRing = kKeys * kD <= 4096 ? 8 : kKeys * kD <= 8192 ? 4 : 2;
+  constexpr int kTileBytes = kKeys * kD * 2, kExtra = kRing >= 4 ? kTileBytes : 16, kMore = kRing == 8 ? kTileBytes : 16;
   // distinct objects, so that the compiler knows that a DMA into one is not read through another
   __shared__ __attribute__((aligned(1024))) uint8_t sK0[kTileBytes], sK1[kTileBytes], sK2[kExtra], sK3[kExtra];
   __shared__ __attribute__((aligned(1024))) uint8_t sV0[kTileBytes], sV1[kTileBytes], sV2[kExtra], sV3[kExtra];
+  __shared__ __attribute__((aligned(1024))) uint8_t sK4[kMore], sK5[kMore], sK6[kMore], sK7[kMore];
+  __shared__ __attribute__((aligned(1024))) uint8_t sV4[kMore], sV5[kMore], sV6[kMore], sV7[kMore];
   __shared__ float sM[kW][32], sL[kW][32];
   const int lane = threadIdx.x & 63, half = lane >> 5, w = wave_id(), rw = w % kRowWaves, kg = w / kRowWaves;
   const int G = a.Hq / a.Hkv, hk = blockIdx.x % a.Hkv;
@@ -450,11 +452,17 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
     if (!again) load_q();   // (on their way together)
     kd.issue(sK1, kKeys);
     vd.issue(sV0, 0);
-    if constexpr (kRing == 4) {
+    if constexpr (kRing >= 4) {
       kd.issue(sK2, 2 * kKeys);
       vd.issue(sV1, kKeys);
     }
-    wait_vm<(kRing == 4 ? 4 : 2) * kL>();   // all but the first tile of keys may still be on their way
+    if constexpr (kRing == 8) {
+      kd.issue(sK3, 3 * kKeys);
+      vd.issue(sV2, 2 * kKeys);
+      kd.issue(sK4, 4 * kKeys);
+      vd.issue(sV3, 3 * kKeys);
+    }
+    wait_vm<kRing * kL>();   // all but the first tile of keys may still be on their way
     block_barrier();
     f32x16_t s0[kB], s1[kB];
     const int mine = kg * kPart;                // first key of this wave's part of tile 0
@@ -462,10 +470,11 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
     if (mine + kPart > w_all) mask_scores<kB>(s0, my_seen - mine);
     float top = top_score<kB>(s0, 0, 16, -INFINITY);   // of the tile whose weights come next
     // Step j: the scores of tile j + 1 (in K1) beside the weights of tile j, then its products (with V0) beside the next
-    // maximum.  The next tiles to load (keys j + 3 and values j + 2, or j + 2 and j + 1) go to Kn and Vn.
+    // maximum.  The next tiles to load (keys j + kRing / 2 + 1 and values j + kRing / 2) go to Kn and Vn, whose tiles were read
+    // before the last barrier, and are read after the next one.
     auto step = [&](int j, f32x16_t (&cur)[kB], f32x16_t (&nxt)[kB], const uint8_t* K1, uint8_t* Kn, uint8_t* V0, uint8_t* Vn) {
       const int j0 = j * kKeys;
-      const NextTiles<kD, kW, kKeys> loads{kd, vd, kd.at(j0 + (kRing == 4 ? 3 : 2) * kKeys), vd.at(j0 + kRing / 2 * kKeys), Kn, Vn};
+      const NextTiles<kD, kW, kKeys> loads{kd, vd, kd.at(j0 + (kRing / 2 + 1) * kKeys), vd.at(j0 + kRing / 2 * kKeys), Kn, Vn};
       if (again) {
         zero_nonfinite<kD, kW, kKeys>(V0);
         __syncthreads();
@@ -490,16 +499,34 @@ __global__ void __launch_bounds__(512, 2) attn_prompt_kernel(PromptArgs a) {
       top = -INFINITY;
       products_and_top<kD, kB>(V0 + part, va, p, st, nxt, top, v);
     };
-    // Before a step, K of the next tile and V of this one have landed: this wave's loads, and every wave's after the
-    // barrier, which also ends all reads of the stages that are loaded next.  With four stages one barrier serves two
-    // steps, which lets the two waves of a SIMD drift apart: one's weights then run beside the other's products.
+    // A barrier every kRing / 2 steps: the tiles that those steps read have landed, this wave's loads by the wait and every
+    // wave's after the barrier, which also ends all reads of the stages that are loaded next.  Between barriers the two
+    // waves of a SIMD may drift apart: one's weights then run beside the other's products.
     auto sync = [&] {
       wait_vm<0>();
       block_barrier();
     };
     for (int j = 0;;) {
       sync();
-      if constexpr (kRing == 4) {
+      if constexpr (kRing == 8) {
+        step(j, s0, s1, sK1, sK5, sV0, sV4);
+        if (++j == tiles) break;
+        step(j, s1, s0, sK2, sK6, sV1, sV5);
+        if (++j == tiles) break;
+        step(j, s0, s1, sK3, sK7, sV2, sV6);
+        if (++j == tiles) break;
+        step(j, s1, s0, sK4, sK0, sV3, sV7);
+        if (++j == tiles) break;
+        sync();
+        step(j, s0, s1, sK5, sK1, sV4, sV0);
+        if (++j == tiles) break;
+        step(j, s1, s0, sK6, sK2, sV5, sV1);
+        if (++j == tiles) break;
+        step(j, s0, s1, sK7, sK3, sV6, sV2);
+        if (++j == tiles) break;
+        step(j, s1, s0, sK0, sK4, sV7, sV3);
+        if (++j == tiles) break;
+      } else if constexpr (kRing == 4) {
         step(j, s0, s1, sK1, sK3, sV0, sV2);
         if (++j == tiles) break;
         step(j, s1, s0, sK2, sK0, sV1, sV3);
