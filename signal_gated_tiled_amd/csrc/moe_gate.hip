@@ -126,13 +126,33 @@ template <int kTop, int kM> __device__ __forceinline__ void sort_top(double (&s)
   }
 }
 
-// The heads of the list that won move up.
-template <int kTop, int kAt = 0, int kM> __device__ __forceinline__ void move_up(double (&s)[kM], bool won) {
-  if constexpr (kAt + 1 < kTop) {
+// The kN heads of the list that won move up.
+template <int kN, int kAt = 0, int kM> __device__ __forceinline__ void move_up(double (&s)[kM], bool won) {
+  if constexpr (kAt + 1 < kN) {
     s[kAt] = won ? s[kAt + 1] : s[kAt];
-    move_up<kTop, kAt + 1>(s, won);
+    move_up<kN, kAt + 1>(s, won);
   } else {
     s[kAt] = won ? 0. : s[kAt];
+  }
+}
+
+// Choice i of a token: the largest of its lanes' heads; then the winner's kN heads move up.  Lane i keeps it.
+template <int kL, int kSlots, int kN, int kM> __device__ __forceinline__ int choose(double (&s)[kM], int j) {
+  const int e = expert_of(over_token<kL>(s[0], larger));
+  move_up<kN>(s, (uint32_t)e / kSlots == (uint32_t)j);
+  return e;
+}
+
+// Choices i = kTop - kN, ... of k <= kTop: before choice i no more than kTop - i heads of a list can still be chosen.
+template <int kL, int kSlots, int kN, int kTop, int kM>
+__device__ __forceinline__ void choose_few(double (&s)[kM], int k, int j, int& pick) {
+  if constexpr (kN > 0) {
+    constexpr int i = kTop - kN;
+    if (i < k) {
+      const int e = choose<kL, kSlots, kN>(s, j);
+      pick = j == i ? e : pick;
+      choose_few<kL, kSlots, kN - 1, kTop>(s, k, j, pick);
+    }
   }
 }
 
@@ -165,8 +185,8 @@ __device__ __forceinline__ float logit(const GateArgs& a, int64_t t, int e) {
 // Waves of a workgroup (see the launch rule).
 template <int kL> constexpr int waves_of() { return kL == 16 ? 4 : 1; }
 
-// kL lanes per token, kSlots experts per lane, of which at most kTop are chosen; kPicks choices per lane at most.
-template <int kL, int kSlots, int kTop, int kPicks>
+// kL lanes per token, kSlots experts per lane, of which at most kTop are chosen; kPicks choices per lane at most; kFew: at most kTop choices in all.
+template <int kL, int kSlots, int kTop, int kPicks, bool kFew>
 __global__ void __launch_bounds__(64 * waves_of<kL>()) moe_gate_kernel(GateArgs a) {
   constexpr int kWaves = waves_of<kL>(), kTokens = 64 / kL;   // tokens of a wave
   __shared__ float sc[kWaves * kTokens][kL * kSlots + 1];
@@ -326,13 +346,14 @@ __global__ void __launch_bounds__(64 * waves_of<kL>()) moe_gate_kernel(GateArgs 
 
   int pick[kPicks] = {};   // lane j keeps choices j, j + kL, ...
   sort_top<kTop>(c);
-  for (int i = 0; i < a.k; ++i) {
-    const double m = over_token<kL>(c[0], larger);
-    const int e = expert_of(m);
-    const bool won = (uint32_t)e / kSlots == (uint32_t)j;
-    move_up<kTop>(c, won);
+  if constexpr (kFew) {
+    choose_few<kL, kSlots, kTop, kTop>(c, a.k, j, pick[0]);
+  } else {
+    for (int i = 0; i < a.k; ++i) {
+      const int e = choose<kL, kSlots, kTop>(c, j);
 #pragma unroll
-    for (int r = 0; r < kPicks; ++r) pick[r] = j + kL * r == i ? e : pick[r];
+      for (int r = 0; r < kPicks; ++r) pick[r] = j + kL * r == i ? e : pick[r];
+    }
   }
 
   float w[kPicks], sum = 0.f;
@@ -354,21 +375,22 @@ __global__ void __launch_bounds__(64 * waves_of<kL>()) moe_gate_kernel(GateArgs 
     }
 }
 
-template <int kL, int kSlots, int kTop, int kPicks>
+template <int kL, int kSlots, int kTop, int kPicks, bool kFew>
 hipError_t launch(const GateArgs& a, hipStream_t stream) {
   constexpr int kWaves = waves_of<kL>(), kTokens = kWaves * 64 / kL;
   const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(64 * kWaves);
-  moe_gate_kernel<kL, kSlots, kTop, kPicks><<<grid, block, 0, stream>>>(a);
+  moe_gate_kernel<kL, kSlots, kTop, kPicks, kFew><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <int kL, int kSlots>
 hipError_t launch_lanes(const GateArgs& a, hipStream_t stream) {
   constexpr int kAll = (64 + kL - 1) / kL;   // choices per lane at most
-  if constexpr (kSlots > 8)   // only the 8 largest of a lane can be chosen: 16381 x 256 9.7 us, sorting all 16 12.5
-    if (a.k <= 8) return launch<kL, kSlots, 8, 1>(a, stream);
-  if (a.k <= kL) return launch<kL, kSlots, kSlots, 1>(a, stream);
-  return launch<kL, kSlots, kSlots, kAll>(a, stream);
+  // up to 8 choices: only the 8 largest of a lane can be among them (16381 x 256 9.7 us, sorting all 16 12.5)
+  if constexpr (kSlots >= 8)
+    if (a.k <= 8) return launch<kL, kSlots, 8, 1, true>(a, stream);
+  if (a.k <= kL) return launch<kL, kSlots, kSlots, 1, false>(a, stream);
+  return launch<kL, kSlots, kSlots, kAll, false>(a, stream);
 }
 
 }  // namespace
