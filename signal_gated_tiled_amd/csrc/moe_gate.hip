@@ -60,6 +60,21 @@ __device__ __forceinline__ double larger(double a, double b) {
   return m;
 }
 
+// f of the values 16 (or 32) lanes apart, in both: a swap of a value with itself leaves the even rows' (the lower half's)
+// values in its first result everywhere and the others' in its second.
+template <bool kHalves, class F> __device__ __forceinline__ float over_rows(float v, F f) {
+  const uint32_t u = __float_as_uint(v);
+  const auto r = kHalves ? __builtin_amdgcn_permlane32_swap(u, u, false, false) : __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <bool kHalves, class F> __device__ __forceinline__ double over_rows(double v, F f) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+  const auto l = kHalves ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false) : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+  const auto h = kHalves ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false) : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+  return f(__builtin_bit_cast(double, ((uint64_t)h[0] << 32) | l[0]), __builtin_bit_cast(double, ((uint64_t)h[1] << 32) | l[1]));
+}
+
 // Reduction over a token's kL lanes, the same in each: quad swaps, half-row and row mirrors, then the four rows.
 template <int kL, class T, class F> __device__ __forceinline__ T over_token(T v, F f) {
   v = f(v, dpp<0xB1>(v));
@@ -67,8 +82,8 @@ template <int kL, class T, class F> __device__ __forceinline__ T over_token(T v,
   v = f(v, dpp<0x141>(v));
   v = f(v, dpp<0x140>(v));
   if constexpr (kL == 64) {
-    v = f(v, __shfl_xor(v, 16));
-    v = f(v, __shfl_xor(v, 32));
+    v = over_rows<false>(v, f);
+    v = over_rows<true>(v, f);
   }
   return v;
 }
