@@ -43,49 +43,11 @@ __device__ __forceinline__ int expert_of(double p) {
   return (int)(kLast - ((uint32_t)__builtin_bit_cast(uint64_t, p) & 0x3FFFFFFFu));
 }
 
-template <int kCtrl> __device__ __forceinline__ double dpp(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, 0xF, 0xF, true);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, true);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-template <int kCtrl> __device__ __forceinline__ float dpp(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xF, 0xF, true));
-}
-
 // The bare instruction: fmax would first quieten NaNs that cannot be here, at three times the cost.
 __device__ __forceinline__ double larger(double a, double b) {
   double m;
   asm("v_max_f64 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
   return m;
-}
-
-// f of the values 16 (or 32) lanes apart, in both: a swap of a value with itself leaves the even rows' (the lower half's)
-// values in its first result everywhere and the others' in its second.
-template <bool kHalves, class F> __device__ __forceinline__ float over_rows(float v, F f) {
-  const uint32_t u = __float_as_uint(v);
-  const auto r = kHalves ? __builtin_amdgcn_permlane32_swap(u, u, false, false) : __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-template <bool kHalves, class F> __device__ __forceinline__ double over_rows(double v, F f) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
-  const auto l = kHalves ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false) : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
-  const auto h = kHalves ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false) : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
-  return f(__builtin_bit_cast(double, ((uint64_t)h[0] << 32) | l[0]), __builtin_bit_cast(double, ((uint64_t)h[1] << 32) | l[1]));
-}
-
-// Reduction over a token's kL lanes, the same in each: quad swaps, half-row and row mirrors, then the four rows.
-template <int kL, class T, class F> __device__ __forceinline__ T over_token(T v, F f) {
-  v = f(v, dpp<0xB1>(v));
-  v = f(v, dpp<0x4E>(v));
-  v = f(v, dpp<0x141>(v));
-  v = f(v, dpp<0x140>(v));
-  if constexpr (kL == 64) {
-    v = over_rows<false>(v, f);
-    v = over_rows<true>(v, f);
-  }
-  return v;
 }
 
 __device__ __forceinline__ double smaller(double a, double b) {
@@ -153,7 +115,7 @@ template <int kN, int kAt = 0, int kM> __device__ __forceinline__ void move_up(d
 
 // Choice i of a token: the largest of its lanes' heads; then the winner's kN heads move up.  Lane i keeps it.
 template <int kL, int kSlots, int kN, int kM> __device__ __forceinline__ int choose(double (&s)[kM], int j) {
-  const int e = expert_of(over_token<kL>(s[0], larger));
+  const int e = expert_of(over_lanes<kL>(s[0], larger));
   move_up<kN>(s, (uint32_t)e / kSlots == (uint32_t)j);
   return e;
 }
@@ -243,14 +205,14 @@ __global__ void __launch_bounds__(64 * waves_of<kL>()) moe_gate_kernel(GateArgs 
   } else {
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) top = fmaxf(top, x[q]);
-    top = over_token<kL>(top, [](float u, float v) { return fmaxf(u, v); });
+    top = over_lanes<kL>(top, [](float u, float v) { return fmaxf(u, v); });
     float total = 0.f;
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) {
       by[q] = weight(x[q], top);
       total += by[q];
     }
-    total = over_token<kL>(total, [](float u, float v) { return u + v; });
+    total = over_lanes<kL>(total, [](float u, float v) { return u + v; });
     inv = total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f;
 #pragma unroll
     for (int q = 0; q < kSlots; ++q) by[q] *= inv;
@@ -336,7 +298,7 @@ __global__ void __launch_bounds__(64 * waves_of<kL>()) moe_gate_kernel(GateArgs 
       double m = g[0];
 #pragma unroll
       for (int r = 1; r < kR; ++r) m = larger(m, g[r]);
-      m = over_token<kL>(m, larger);
+      m = over_lanes<kL>(m, larger);
       const int best = expert_of(m);
       kept |= 1ull << (best & 63);
 #pragma unroll
@@ -379,7 +341,7 @@ __global__ void __launch_bounds__(64 * waves_of<kL>()) moe_gate_kernel(GateArgs 
     if (j + kL * r >= a.k) w[r] = 0.f;
     sum += w[r];
   }
-  sum = over_token<kL>(sum, [](float u, float v) { return u + v; });
+  sum = over_lanes<kL>(sum, [](float u, float v) { return u + v; });
   const float f = a.renormalize ? (sum > 0.f ? a.scale / sum : 0.f) : a.scale;
   if (!live) return;
 #pragma unroll

@@ -112,16 +112,12 @@ __device__ __forceinline__ void write_vec(void* p, int dtype, int64_t at, int n,
     }
 }
 
-// Sum and largest magnitude over kLanes neighbouring lanes.
+// Sum and largest magnitude over 16 or 64 neighbouring lanes.
 template <int kLanes> __device__ __forceinline__ float sum_over(float v) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return over_lanes<kLanes>(v, [](float x, float y) { return x + y; });
 }
 template <int kLanes> __device__ __forceinline__ float abs_max_over(float v) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) v = abs_max(v, __shfl_xor(v, o));
-  return v;
+  return over_lanes<kLanes>(v, [](float x, float y) { return abs_max(x, y); });
 }
 
 // A row is kLanes neighbouring lanes', or with kLanes = 0 the workgroup's.
