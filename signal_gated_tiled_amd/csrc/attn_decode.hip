@@ -103,14 +103,24 @@ Divisor divisor(int d) {
   return {(uint32_t)((two + d - 1) / d), s, d};
 }
 
+// v of another lane, in the rows of kRows, zero elsewhere and where there is none.
+template <int kCtrl, int kRows> __device__ __forceinline__ int64_t shifted(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, kCtrl, kRows, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)((uint64_t)v >> 32), kCtrl, kRows, 0xF, false);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // Inclusive prefix sum over the workgroup and its total; `red` holds kWaves words.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
+  // inside each row of 16 lanes (shifts bring in zeros), then rows 1 and 3 add the last lane of the row before, rows 2 and 3
+  // that of the lower half
+  v += shifted<0x111, 0xF>(v);
+  v += shifted<0x112, 0xF>(v);
+  v += shifted<0x114, 0xF>(v);
+  v += shifted<0x118, 0xF>(v);
+  v += shifted<0x142, 0xA>(v);
+  v += shifted<0x143, 0xC>(v);
   __syncthreads();
   if (lane == 63) red[w] = v;
   __syncthreads();
@@ -300,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
         for (int h = 0; h < kS; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j) t = fmaxf(t, s[i][h][j]);
-        t = fmaxf(t, __shfl_xor(t, 16));
-        t = fmaxf(t, __shfl_xor(t, 32));
+        t = over_rows<false>(t, [](float x, float y) { return fmaxf(x, y); });
+        t = over_rows<true>(t, [](float x, float y) { return fmaxf(x, y); });
         if (__any(t > lim[i])) {
           const float mn = fmaxf(m[i], t), mcn = mn == -INFINITY ? 0.f : mn * c2;
           const float f = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mc[i] - mcn);
@@ -405,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
     const __amdgpu_buffer_rsrc_t rp = make_rsrc(part, kSlotFloats * 4);
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
-      l[i] += __shfl_xor(l[i], 16);
-      l[i] += __shfl_xor(l[i], 32);
+      l[i] = over_rows<false>(l[i], [](float x, float y) { return x + y; });
+      l[i] = over_rows<true>(l[i], [](float x, float y) { return x + y; });
       if (jg == 0) {
         sM[w][16 * i + jc] = m[i] == -INFINITY ? -INFINITY : mc[i];
         sL[w][16 * i + jc] = l[i];
