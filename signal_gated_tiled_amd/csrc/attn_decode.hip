@@ -25,9 +25,9 @@
 //
 // Rounding.  Scores, maxima, sums, parts and joins are fp32; the weights are two bf16 parts (16 bits of each weight).
 //
-// Measured: 4 sequences of 90000 to 131072 tokens, 64 query heads on 8, D 128, 303 us (1.75 GB at 5.8 TB/s; a 2 GiB copy
-// reaches 4.9 here); 128 sequences of 1 to 16000, 8 heads on one, 32 us (117 MB at 3.6 TB/s, of which about 8 us are the chain of
-// launch, lengths, page ids, first tile and joins); one of 777 9.8 us, that chain alone.
+// Measured: 4 sequences of 90000 to 131072 tokens, 64 query heads on 8, D 128, 301 us (1.75 GB at 5.8 TB/s; a 2 GiB copy
+// reaches 4.9 here); 128 sequences of 1 to 16000, 8 heads on one, 32 us (117 MB at 3.6 TB/s, of which about 7 us are the chain of
+// launch, lengths, page ids, first tile and joins); one of 777 9.4 us, that chain alone.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -43,14 +43,14 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRing = 4;                      // LDS stages of a wave
 constexpr int kGrid = 256;                   // workgroups: one on each CU (128 KiB of LDS)
-// Tiles of a range at least: one for each wave.  (us at 4 / 8 / 16 tiles, one sequence, 8 query heads and 1 key head:
-// 100 keys 9.1 / 8.1 / 8.1, 777 keys 10.5 / 11.2 / 11.7, 4096 keys 13.5 / 14.1 / 13.0, 16384 keys 15.4 / 14.8 / 15.7)
-constexpr int kMinTiles = 4;
+// Tiles of a range at least: two for each wave.  (us at 4 / 8 / 16 tiles, one sequence, 8 query heads and 1 key head:
+// 128 keys 8.1 / 7.0 / 7.1, 777 keys 9.7 / 9.4 / 10.1, 2000 keys 12.2 / 10.5 / 11.5, 4000 keys 12.4 / 12.9 / 11.8)
+constexpr int kMinTiles = 8;
 // What starting and joining a problem costs a workgroup, in tiles.  (us at 0 / 8 / 24 / 48: 128 sequences of 1 to 16000
-// keys 63 / 39 / 34 / 35, 64 of 1000 with 4 key heads 49 / 40 / 37 / 37, 256 of 1 to 300 20.5 / 13.9 / 13.3 / 13.4)
+// keys 60 / 38 / 33 / 34, 64 of 1000 with 4 key heads 44 / 36.5 / 35 / 35, 256 of 1 to 300 18.5 / 12.2 / 12.2 / 12.2)
 constexpr int kProblemCost = 24;
 // Parts joined at once; a problem has at most kFan^2, one in each workgroup.  (One sequence of 131072 keys and 1 key head:
-// 26.4 us in 256 parts and two levels; 43 when cut into 64 parts joined by one workgroup in four rounds.)
+// 24 us in 256 parts and two levels; 43 when cut into 64 parts joined by one workgroup in four rounds.)
 constexpr int kFan = 16;
 constexpr int kMaxRows = 32;                 // query heads of a chunk
 constexpr int kSlotStats = kMaxRows * 128;    // one part: outputs, maxima and sums, then the maxima and sums of kFan joined
@@ -519,7 +519,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       };
       const int first = mine / kFan * kFan, n = min(kFan, n_parts - first);
       if (is_last(counters + slot_of(first), n)) {
+        // (a load that finds no part costs time too: 7 parts joined as 16 10.2 us, as 8 9.4)
         if (n_parts <= 4) join(std::integral_constant<int, 4>(), first, 1, n, kSlotStats, true);
+        else if (n_parts <= 8) join(std::integral_constant<int, 8>(), first, 1, n, kSlotStats, true);
         else join(std::integral_constant<int, kFan>(), first, 1, n, kSlotStats, n_parts <= kFan);
         const int groups = (n_parts + kFan - 1) / kFan;
         if (groups > 1 && is_last(counters + 2 * kGrid + slot_of(0), groups))

@@ -12,9 +12,9 @@
 // held it moves up.  The chosen experts' scores are computed again from their logits
 // at the end, which costs one small gather instead of carrying every score along.
 //
-// Scores, sums and weights are fp32.  Measured: 16381 x 256 in groups with a bias 12.0 us (17.8 MB, 1.5 TB/s; about 1150
-// vector instructions per wave of four tokens, on which the vector units spend some 9 of them), 16381 x 64 softmax 4.9, 16 tokens 3.3: the
-// launch, two memory latencies and eight dependent rounds.
+// Scores, sums and weights are fp32.  Measured: 16381 x 256 in groups with a bias 11.4 us (17.8 MB, 1.6 TB/s; about 1060
+// vector instructions per wave of four tokens, on which the vector units spend most of it), 16381 x 64 softmax 4.8, 16
+// tokens 3.4: the launch, two memory latencies and eight dependent rounds.
 #include <hip/hip_runtime.h>
 
 #include "elem.hpp"
@@ -376,7 +376,7 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t stream) {
   // 16 lanes take a token of up to 256 experts, so that a round's exchanges serve four tokens (16381 x 256 9.7 us, by whole
   // waves 14.2; x 64 4.9 and 14.3); more experts take a whole wave, in workgroups of one (16 x 1024 in groups 6.2 us, in
   // workgroups of four 8.1: the waves wait for each other's dispatch).  As few slots per lane as hold them: 16381 x 64
-  // 4.9 us, with 16 slots 9.0; 16381 x 512 20.8 and 30.5.
+  // 4.9 us, with 16 slots 9.0; 16381 x 512 20.8 and 30.5.  (All before the rounds' lists grew shorter.)
   if (a.E <= 64) return launch_lanes<16, 4>(a, stream);
   if (a.E <= 128) return launch_lanes<16, 8>(a, stream);
   if (a.E <= 256) return launch_lanes<16, 16>(a, stream);

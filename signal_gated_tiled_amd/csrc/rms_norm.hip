@@ -12,7 +12,7 @@
 // vector they would begin.
 //
 // Measured: 2048 x 8192 fp32 rows with a bf16 residual and output 29.7 us (168 MB at 5.6 TB/s; a 2 GiB copy reaches 4.9
-// here), 8191 x 5120 bf16 to 8 bits 60.9 us (295 MB at 4.8 TB/s).  One row of 8192 takes 3.6 us, three times the
+// here), 8191 x 5120 bf16 to 8 bits 60 us (295 MB at 4.9 TB/s).  One row of 8192 takes 3.4 us, three times the
 // memory's latency and the launch.  Stores past the L2 were worth 37.5 -> 34.7 and 69.4 -> 64.6 us, one or two vectors per
 // thread instead of four the rest.
 #include <hip/hip_runtime.h>
@@ -220,13 +220,13 @@ hipError_t launch(const NormArgs& a, int vecs, hipStream_t stream) {
 
 template <bool kF32>
 hipError_t launch_type(const NormArgs& a, hipStream_t stream) {
-  // Rows of up to 128 elements: 16 lanes each, or most of a wave would idle (65536 x 128: 12.0 us, by whole waves 21.6).
-  // Up to 512: a wave each, without barriers (1 x 512: 2.9 us, and 2.9 by a workgroup; 65536 x 128 bf16 21.8 and 22.4).
+  // Rows of up to 128 elements: 16 lanes each, or most of a wave would idle (65536 x 128: 11.7 us, by whole waves 20.1).
+  // Up to 512: a wave each, without barriers (1 x 512: 2.7 us, 2.8 by a workgroup; 65536 x 128 bf16 21.8 and 22.4).
   // Longer rows take a workgroup and as few vectors per thread as fit, the rest of the latency hidden by other rows:
-  // 1 x 8192 at 1 / 2 / 4 vectors 3.6 / 4.1 / 5.8 us, 8191 x 2048 21.6 / 22.3 / 26.2.  Past 4096 elements one vector
+  // 1 x 8192 at 1 / 2 / 4 vectors 3.4 / 3.9 / 5.7 us, 8191 x 2048 21.8 / 23.0 / 25.5.  Past 4096 elements one vector
   // each makes workgroups of 9 to 16 waves, of which few fit a CU's 32; with rows to spare two are better: 8191 x 5120
-  // bf16 65.6 / 61.4, to 8 bits 67.1 / 61.7, 1024 x 5120 9.5 / 8.3; at 8192 even (bf16 90.6 / 92.8, 8 bits 90.9 / 85.0);
-  // 256 rows of 5120 4.4 / 5.0.
+  // bf16 65.0 / 60.5, to 8 bits 65.0 / 59.6, 1024 x 5120 9.2 / 8.1; at 8192 even (bf16 90.4 / 92.2, 8 bits 88.5 / 84.0);
+  // 256 rows of 5120 3.9 / 4.5.
   const int vecs = (a.H + kVec - 1) / kVec;
   if (vecs <= 16) return launch_lanes<kF32, 16>(a, stream);
   if (vecs <= 64) return launch_lanes<kF32, 64>(a, stream);
