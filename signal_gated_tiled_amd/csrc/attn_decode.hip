@@ -26,7 +26,7 @@
 // Rounding.  Scores, maxima, sums, parts and joins are fp32; the weights are two bf16 parts (16 bits of each weight).
 //
 // Measured: 4 sequences of 90000 to 131072 tokens, 64 query heads on 8, D 128, 301 us (1.75 GB at 5.8 TB/s; a 2 GiB copy
-// reaches 4.9 here); 128 sequences of 1 to 16000, 8 heads on one, 32 us (117 MB at 3.6 TB/s, of which about 7 us are the chain of
+// reaches 4.9 here); 128 sequences of 1 to 16000, 8 heads on one, 31 us (117 MB at 3.8 TB/s, of which about 7 us are the chain of
 // launch, lengths, page ids, first tile and joins); one of 777 9.4 us, that chain alone.
 #include <hip/hip_runtime.h>
 

@@ -27,10 +27,10 @@
 //
 // What bounds it: a wave's step of 64 keys at D 128 is 32 matrix instructions (1024 cycles) beside about 170 vector
 // instructions (32 exponentials of 8 cycles, 16 packings of 8, the rest 3 to 5), and with long prompts the power limit.
-// Measured: one causal prompt of 16384 tokens, 8 query heads on one key head, D 128, 489 us (1.1 PFLOP/s; a large matrix
-// product of this card's library reaches 1.5), matrix units busy 53% of the cycles, vector units 41%; 16 prompts of 1 to
+// Measured: one causal prompt of 16384 tokens, 8 query heads on one key head, D 128, 490 us (1.1 PFLOP/s; a large matrix
+// product of this card's library reaches 1.5), matrix units busy 56% of the cycles, vector units 43%; 16 prompts of 1 to
 // 1500 tokens 29 us, bound by the longest one's chain of steps of about 1.6 us; 3 pieces of 300 to 700 tokens behind 6000,
-// 16 heads on 4, D 64, 72 us (0.64 PFLOP/s: half the matrix work per exponential).
+// 16 heads on 4, D 64, 70 us (0.65 PFLOP/s: half the matrix work per exponential).
 //
 // Values of keys a row does not see get weight 0, which a NaN or infinity
 // would survive.  Keys past a sequence's end read as zeros; a later key inside

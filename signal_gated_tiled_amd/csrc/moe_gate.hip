@@ -12,7 +12,7 @@
 // held it moves up.  The chosen experts' scores are computed again from their logits
 // at the end, which costs one small gather instead of carrying every score along.
 //
-// Scores, sums and weights are fp32.  Measured: 16381 x 256 in groups with a bias 11.4 us (17.8 MB, 1.6 TB/s; about 1060
+// Scores, sums and weights are fp32.  Measured: 16381 x 256 in groups with a bias 11.2 to 12.1 us (17.8 MB, 1.5 TB/s; about 1075
 // vector instructions per wave of four tokens, on which the vector units spend most of it), 16381 x 64 softmax 4.8, 16
 // tokens 3.4: the launch, two memory latencies and eight dependent rounds.
 #include <hip/hip_runtime.h>
@@ -363,7 +363,7 @@ hipError_t launch(const GateArgs& a, hipStream_t stream) {
 template <int kL, int kSlots>
 hipError_t launch_lanes(const GateArgs& a, hipStream_t stream) {
   constexpr int kAll = (64 + kL - 1) / kL;   // choices per lane at most
-  // up to 8 choices: only the 8 largest of a lane can be among them (16381 x 256 9.7 us, sorting all 16 12.5)
+  // up to 8 choices: only the 8 largest of a lane can be among them (16381 x 256 9.2 us, sorting all 16 12.6)
   if constexpr (kSlots >= 8)
     if (a.k <= 8) return launch<kL, kSlots, 8, 1, true>(a, stream);
   if (a.k <= kL) return launch<kL, kSlots, kSlots, 1, false>(a, stream);
@@ -373,10 +373,10 @@ hipError_t launch_lanes(const GateArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_moe_gate(const GateArgs& a, hipStream_t stream) {
-  // 16 lanes take a token of up to 256 experts, so that a round's exchanges serve four tokens (16381 x 256 9.7 us, by whole
-  // waves 14.2; x 64 4.9 and 14.3); more experts take a whole wave, in workgroups of one (16 x 1024 in groups 6.2 us, in
-  // workgroups of four 8.1: the waves wait for each other's dispatch).  As few slots per lane as hold them: 16381 x 64
-  // 4.9 us, with 16 slots 9.0; 16381 x 512 20.8 and 30.5.  (All before the rounds' lists grew shorter.)
+  // 16 lanes take a token of up to 256 experts, so that a round's exchanges serve four tokens (16381 x 256 9.2 us, by whole
+  // waves 15.8; x 64 4.8 and 15.7); more experts take a whole wave, in workgroups of one (16381 x 512 18.5 us, 16 x 1024 in
+  // groups 5.4, in workgroups of four 19.0 and 5.6).  As few slots per lane as hold them: 16381 x 64 4.8 us, with 16
+  // slots 8.2; 16381 x 512 18.5 and 27.1.
   if (a.E <= 64) return launch_lanes<16, 4>(a, stream);
   if (a.E <= 128) return launch_lanes<16, 8>(a, stream);
   if (a.E <= 256) return launch_lanes<16, 16>(a, stream);

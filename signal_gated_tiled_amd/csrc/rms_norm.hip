@@ -12,7 +12,7 @@
 // vector they would begin.
 //
 // Measured: 2048 x 8192 fp32 rows with a bf16 residual and output 29.7 us (168 MB at 5.6 TB/s; a 2 GiB copy reaches 4.9
-// here), 8191 x 5120 bf16 to 8 bits 60 us (295 MB at 4.9 TB/s).  One row of 8192 takes 3.4 us, three times the
+// here), 8191 x 5120 bf16 to 8 bits 59 us (295 MB at 5.0 TB/s).  One row of 8192 takes 3.4 us, three times the
 // memory's latency and the launch.  Stores past the L2 were worth 37.5 -> 34.7 and 69.4 -> 64.6 us, one or two vectors per
 // thread instead of four the rest.
 #include <hip/hip_runtime.h>
