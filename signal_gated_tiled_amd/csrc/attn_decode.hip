@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
       if (a.lse && at == 0) a.lse[(int64_t)b * a.Hq + h0 + r] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
     };
 
-    // join the waves: each scales its output to the common maximum and leaves it in its stage
+    // join the waves: each leaves its output in its stage, to be brought to the common maximum as it is added
     const int jl = fresh_lane(), jt = w * 64 + jl, jg = jl >> 4, jc = jl & 15;
     const bool whole = ta == 0 && tb == n_tiles;
     const int64_t w_first = start >= u0 ? (int64_t)blockIdx.x : quotient(start, chunk);
@@ -422,16 +422,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
         sL[w][16 * i + jc] = l[i];
       }
     }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kNQ; ++i) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < kWaves; ++x) M = fmaxf(M, sM[x][16 * i + jc]);
-      const float f = m[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mc[i] - M);
       f32x4_t* mine = reinterpret_cast<f32x4_t*>(&sA[w]) + jc * (kD / 4);
 #pragma unroll
-      for (int n = 0; n < kNB; ++n) mine[(4 * n + jg) ^ jc] = o[i][n] * f;
+      for (int n = 0; n < kNB; ++n) mine[(4 * n + jg) ^ jc] = o[i][n];
       __syncthreads();
       for (int e = jt; e < 16 * kD / 4; e += kThreads) {
         const int row = e / (kD / 4), at = e % (kD / 4), r = 16 * i + row;
@@ -442,9 +437,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_kernel(DecodeArgs a, 
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < kWaves; ++x) {
-          v += reinterpret_cast<const f32x4_t*>(&sA[x])[row * (kD / 4) + (at ^ row)];
-          const float mx = sM[x][r], lx = sL[x][r];
-          L += mx == -INFINITY ? lx : lx * __builtin_amdgcn_exp2f(mx - Mr);
+          const float mx = sM[x][r], lx = sL[x][r], f = mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(mx - Mr);
+          v += reinterpret_cast<const f32x4_t*>(&sA[x])[row * (kD / 4) + (at ^ row)] * f;
+          L += lx * f;
         }
         if (whole) {
           finish(r, at, v, Mr, L);
